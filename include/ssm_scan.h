@@ -406,6 +406,184 @@ SSM_API int ssm_cp_fill_tail(const ssm_desc_t *d, void *x, void *dt, void *B, vo
 SSM_API int ssm_cp_write_adjoint(const ssm_desc_t *d, const void *x, const void *B,
                                  const float *dw_end, void *dx, void *dB, void *stream);
 
+/*
+ * ---- The layer around the mixer ------------------------------------------------------
+ * Operators a layer needs next to its scan.  They take their own small descriptors;
+ * strides are element strides, the innermost dimension of every tensor is dense, inputs
+ * may be broadcast (stride 0), outputs may not.  Caller-owned memory, the caller's
+ * stream and the error codes of the calls above; the descriptors' reserved fields must
+ * be 0.  Nothing is launched for an empty problem (no rows, batch or tokens) except
+ * where a call says what it then writes.
+ */
+
+/* 8-bit output of ssm_rmsnorm_fwd: e4m3 codes with one fp32 scale per row, or per block
+ * of 128 columns. */
+enum ssm_quant { SSM_QUANT_NONE = 0, SSM_QUANT_ROW = 1, SSM_QUANT_BLOCK = 2 };
+
+/*
+ * Root-mean-square norm of `rows` rows of `dim` values, with the addition of a residual
+ * stream in front of it.  dim up to 2^20.  Row strides (elements): x, residual, r
+ * (the sum), y, y8, dy, dr, dx.
+ */
+typedef struct ssm_rmsnorm_desc {
+    int64_t rows, dim;
+    int64_t stride_x, stride_residual, stride_r, stride_y, stride_y8;
+    int64_t stride_dy, stride_dr, stride_dx;
+    float eps;         /* >= 0 */
+    int32_t dtype_io;  /* enum ssm_dtype of x, residual, r, y, dy, dr, dx */
+    int32_t quant;     /* enum ssm_quant; SSM_QUANT_BLOCK needs dim % 128 == 0 */
+    int32_t reserved_;
+} ssm_rmsnorm_desc_t;
+
+/*
+ *     r = x + residual            (rounded to dtype_io; r = x without a residual)
+ *     rstd = 1 / sqrt(mean(r^2) + eps),   y = r rstd w
+ * x and residual are read, r (may be NULL without a residual) receives the sum, which
+ * may overwrite x or residual.  weight is fp32 [dim] (NULL: ones).  With SSM_QUANT_NONE y
+ * receives the result in dtype_io.  Otherwise y8 receives e4m3 codes and scales (fp32
+ * [rows][1] or [rows][dim / 128], dense) the scale of each row or block:
+ *     scale = max|y| / 448,   code = e4m3(y 448 / max|y|)     (y in fp32, not rounded first)
+ * so that code * scale approximates y; a block of zeros has codes and scale 0, one that
+ * holds a NaN or an infinity has that scale.  y may then be NULL, or receives the
+ * unquantised result too.  rstd (fp32 [rows], may be NULL) is what ssm_rmsnorm_bwd reads.
+ */
+SSM_API int ssm_rmsnorm_fwd(const ssm_rmsnorm_desc_t *d, const void *x, const void *residual,
+                            const float *weight, void *r, void *y, void *y8, float *scales,
+                            float *rstd, void *stream);
+
+/* Bytes of device workspace ssm_rmsnorm_bwd needs for dweight (0 for a bad descriptor or
+ * an empty problem). */
+SSM_API size_t ssm_rmsnorm_workspace_size(const ssm_rmsnorm_desc_t *d);
+
+/*
+ * Gradients for dy, the gradient of y, and dr (may be NULL), that of r through the
+ * residual stream; r and rstd as the forward left them:
+ *     dx = rstd (w dy - xhat mean(w dy xhat)) + dr,   xhat = r rstd,
+ *     dweight = sum over the rows of dy xhat
+ * dx is the gradient of x and of residual alike; it may overwrite dy or dr.  dweight (fp32
+ * [dim]) may be NULL, as then may workspace; its sum runs in a fixed order (deterministic).
+ * Without rows dweight is set to zero.
+ */
+SSM_API int ssm_rmsnorm_bwd(const ssm_rmsnorm_desc_t *d, const void *dy, const void *r,
+                            const float *weight, const float *rstd, const void *dr, void *dx,
+                            float *dweight, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/* Order of a rotary pair in its head: (i, i + rot_dim / 2), or (2 i, 2 i + 1). */
+enum ssm_rope_layout { SSM_ROPE_HALF = 0, SSM_ROPE_PAIRS = 1 };
+/* Frequencies for contexts longer than those trained on (ssm_rope_frequencies):
+ * SSM_ROPE_LINEAR divides every frequency by the factor (positions interpolated);
+ * SSM_ROPE_NTK raises the base to base * factor^(rot_dim / (rot_dim - 2));
+ * SSM_ROPE_BANDS keeps the pairs that turn at least high_turns times within the original
+ * context, divides those that turn at most low_turns times, and blends linearly in the
+ * number of turns between them. */
+enum ssm_rope_scaling { SSM_ROPE_PLAIN = 0, SSM_ROPE_LINEAR = 1, SSM_ROPE_NTK = 2, SSM_ROPE_BANDS = 3 };
+
+/* Queries q and keys k, [batch][seqlen][heads][headdim]; stride_* (batch, time, head). */
+typedef struct ssm_rope_desc {
+    int64_t batch, seqlen, nheads_q, nheads_k, headdim;
+    int64_t rot_dim;   /* even, <= headdim: the first rot_dim values of a head are rotated */
+    int64_t stride_q[3], stride_k[3];           /* of the tensors read */
+    int64_t stride_q_out[3], stride_k_out[3];   /* of the tensors written */
+    int64_t stride_pos[2];                      /* batch, time */
+    float magnitude;   /* factor of the rotated part (1, or the attention factor of a scaling) */
+    int32_t layout;    /* enum ssm_rope_layout */
+    int32_t dtype_io;
+    int32_t reserved_;
+} ssm_rope_desc_t;
+
+/* Host call: the rot_dim / 2 frequencies (radians a position) of a base and a scaling, to
+ * host memory; copy them to the device for the calls below.  factor >= 1; low_turns <
+ * high_turns and original_context are read by SSM_ROPE_BANDS. */
+SSM_API int ssm_rope_frequencies(int64_t rot_dim, double base, int scaling, double factor,
+                                 double low_turns, double high_turns, double original_context,
+                                 double *freq);
+
+/*
+ * Rotary positions: pair j of every head at position m turns by the angle m freq[j],
+ *     (a, b) -> magnitude (a cos - b sin, a sin + b cos),
+ * and the values past rot_dim are copied.  freq is fp64 [rot_dim / 2] on the device, and the
+ * angle is reduced in 64 bits, so far positions lose nothing.  positions (int64, may be
+ * negative) are [batch][seqlen] at stride_pos, or NULL for 0, 1, 2, ...  q or k may be NULL
+ * (with its output).  An output may be its own input (the same address and strides).
+ */
+SSM_API int ssm_rope_fwd(const ssm_rope_desc_t *d, const void *q, const void *k,
+                         const double *freq, const int64_t *positions, void *q_out, void *k_out,
+                         void *stream);
+
+/* Gradient through ssm_rope_fwd: the rotation by the opposite angle, times magnitude; dq
+ * and dk are the gradients of its outputs (at stride_q / stride_k), dq_out and dk_out receive those of
+ * its inputs (at stride_q_out / stride_k_out). */
+SSM_API int ssm_rope_bwd(const ssm_rope_desc_t *d, const void *dq, const void *dk,
+                         const double *freq, const int64_t *positions, void *dq_out,
+                         void *dk_out, void *stream);
+
+/*
+ * Linear attention with a decay for each head: the scan's masked linear attention
+ * (sungsoo.github.io Part 03) with a transition that is one constant of the head, in the
+ * layout of an attention layer.  Per batch row b and head h, with the key and value head
+ * g = h / (nheads / nheads_kv):
+ *     S_t = e^{log_decay[h]} S_{t-1} + k_t v_t^T,   o_t = scale q_t S_t      (S_{-1} = state_in)
+ *   q, dq   [batch][seqlen][nheads][dim_k]       k, dk   [batch][seqlen][nheads_kv][dim_k]
+ *   v, dv   [batch][seqlen][nheads_kv][dim_v]    o, do   [batch][seqlen][nheads][dim_v]
+ *   states  fp32 [batch][nheads][dim_k][dim_v], dense;  log_decay fp32 [nheads], <= 0
+ * (-inf keeps nothing).  lengths (int32 [batch] on the device, NULL: all seqlen) ends row b
+ * after its first lengths[b] tokens (clamped to 0 .. seqlen): the rows behind them are not
+ * read, and those of the outputs are left as they were.  dim_k and dim_v up to 256.
+ * The decays are constants of the head and have no gradient; a learned, per-token
+ * decay is ssm_scan_*.  A value that is not finite in a token of the sequence may reach every
+ * output of its batch row and head.
+ */
+typedef struct ssm_linattn_desc {
+    int64_t batch, seqlen, nheads, nheads_kv, dim_k, dim_v;
+    int64_t stride_q[3], stride_k[3], stride_v[3], stride_o[3];   /* batch, time, head; o: also do */
+    int64_t stride_dq[3], stride_dk[3], stride_dv[3];
+    float scale;
+    int32_t dtype_io;
+    int32_t route;      /* enum ssm_linattn_route */
+    int32_t reserved_;
+} ssm_linattn_desc_t;
+
+/* SSM_LINATTN_AUTO: the tensor-core walk over 128-token chunks where it applies (bf16,
+ * head dims that are multiples of 8 and at most 128, 16-byte aligned tensors and strides),
+ * else the token-by-token recurrence; SSM_LINATTN_RECURRENT: always the latter.  Results
+ * are equal up to rounding. */
+enum ssm_linattn_route { SSM_LINATTN_AUTO = 0, SSM_LINATTN_RECURRENT = 1 };
+
+/* Bytes of device workspace (256-byte aligned, contents arbitrary) that ssm_linattn_fwd
+ * (SSM_PASS_FWD) or ssm_linattn_bwd (SSM_PASS_BWD) needs; 0: none. */
+SSM_API size_t ssm_linattn_workspace_size(const ssm_linattn_desc_t *d, int pass);
+
+/*
+ * Whole sequences.  state_in may be NULL (zero); o (state only) or state_out may be NULL,
+ * not both; state_out may be state_in.  A row of length 0 has state_out = state_in.
+ */
+SSM_API int ssm_linattn_fwd(const ssm_linattn_desc_t *d, const void *q, const void *k,
+                            const void *v, const float *log_decay, const float *state_in,
+                            const int32_t *lengths, void *o, float *state_out, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of sum(do * o) + sum(dstate_out * state_out) (do_; dstate_out may be NULL):
+ *     dq_t = scale S_t do_t,   G_t = scale q_t do_t^T + e^{g} G_{t+1}   (G behind the last
+ *     token: e^{g} G = dstate_out),   dk_t = G_t v_t,   dv_t = G_t^T k_t,
+ *     dstate_in = e^{g} G_0
+ * The states are recomputed; dk and dv sum the heads that share them in a fixed order.
+ * dq, dk and dv are written up to each row's length.  dstate_in may be NULL; it must not be
+ * dstate_out, which two of the sums read.
+ */
+SSM_API int ssm_linattn_bwd(const ssm_linattn_desc_t *d, const void *q, const void *k,
+                            const void *v, const float *log_decay, const float *state_in,
+                            const int32_t *lengths, const void *do_, const float *dstate_out,
+                            void *dq, void *dk, void *dv, float *dstate_in, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* One token (d->seqlen must be 1), the state updated in place: the serving form, equal to
+ * ssm_linattn_fwd over the token up to rounding.  No workspace. */
+SSM_API int ssm_linattn_step(const ssm_linattn_desc_t *d, const void *q, const void *k,
+                             const void *v, const float *log_decay, float *state, void *o,
+                             void *stream);
+
 /* Message describing the last failing call on this host thread ("" if none). */
 SSM_API const char *ssm_scan_last_error(void);
 

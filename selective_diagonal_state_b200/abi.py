@@ -28,7 +28,16 @@ EXPORTED = ["ssm_desc_set_contiguous", "ssm_scan_workspace_size", "ssm_scan_fwd"
             "ssm_scan_step", "ssm_preact_fwd", "ssm_preact_bwd", "ssm_scan_set_wait_limit",
             "ssm_cp_tail_rows", "ssm_cp_segment_transition", "ssm_cp_state_combine",
             "ssm_cp_adjoint_combine", "ssm_cp_fill_tail", "ssm_cp_write_adjoint",
-            "ssm_scan_fwd_gated", "ssm_gate_bwd"]
+            "ssm_scan_fwd_gated", "ssm_gate_bwd",
+            "ssm_rmsnorm_fwd", "ssm_rmsnorm_workspace_size", "ssm_rmsnorm_bwd",
+            "ssm_rope_frequencies", "ssm_rope_fwd", "ssm_rope_bwd",
+            "ssm_linattn_workspace_size", "ssm_linattn_fwd", "ssm_linattn_bwd",
+            "ssm_linattn_step"]
+DTYPE_F32, DTYPE_BF16 = 0, 1
+QUANT_NONE, QUANT_ROW, QUANT_BLOCK = 0, 1, 2
+ROPE_HALF, ROPE_PAIRS = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_BANDS = 0, 1, 2, 3
+LINATTN_AUTO, LINATTN_RECURRENT = 0, 1
 ROUTE_CHUNKED, ROUTE_RANGE_FALLBACK, ROUTE_RECURRENT, ROUTE_SSD, ROUTE_CHANNEL = 0, 1, 2, 3, 4
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -55,6 +64,38 @@ class Desc(ctypes.Structure):
         ("angle_mode", ctypes.c_int32), ("n_static", ctypes.c_int32),
         ("discretization", ctypes.c_int32), ("reserved_", ctypes.c_int32),
     ]
+
+
+class RmsnormDesc(ctypes.Structure):
+    """Mirror of ``ssm_rmsnorm_desc_t``."""
+
+    _fields_ = ([(f, ctypes.c_int64) for f in (
+        "rows", "dim", "stride_x", "stride_residual", "stride_r", "stride_y", "stride_y8",
+        "stride_dy", "stride_dr", "stride_dx")] +
+        [("eps", ctypes.c_float), ("dtype_io", ctypes.c_int32), ("quant", ctypes.c_int32),
+         ("reserved_", ctypes.c_int32)])
+
+
+class RopeDesc(ctypes.Structure):
+    """Mirror of ``ssm_rope_desc_t``."""
+
+    _fields_ = ([(f, ctypes.c_int64) for f in (
+        "batch", "seqlen", "nheads_q", "nheads_k", "headdim", "rot_dim")] +
+        [(f, ctypes.c_int64 * 3) for f in ("stride_q", "stride_k", "stride_q_out",
+                                           "stride_k_out")] +
+        [("stride_pos", ctypes.c_int64 * 2), ("magnitude", ctypes.c_float),
+         ("layout", ctypes.c_int32), ("dtype_io", ctypes.c_int32), ("reserved_", ctypes.c_int32)])
+
+
+class LinattnDesc(ctypes.Structure):
+    """Mirror of ``ssm_linattn_desc_t``."""
+
+    _fields_ = ([(f, ctypes.c_int64) for f in (
+        "batch", "seqlen", "nheads", "nheads_kv", "dim_k", "dim_v")] +
+        [(f, ctypes.c_int64 * 3) for f in ("stride_q", "stride_k", "stride_v", "stride_o",
+                                           "stride_dq", "stride_dk", "stride_dv")] +
+        [("scale", ctypes.c_float), ("dtype_io", ctypes.c_int32), ("route", ctypes.c_int32),
+         ("reserved_", ctypes.c_int32)])
 
 
 _lib = None
@@ -107,6 +148,29 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ssm_cp_fill_tail.restype = ctypes.c_int
     lib.ssm_cp_write_adjoint.argtypes = [ctypes.POINTER(Desc)] + [_vp] * 6
     lib.ssm_cp_write_adjoint.restype = ctypes.c_int
+    norm, rope, la = (ctypes.POINTER(t) for t in (RmsnormDesc, RopeDesc, LinattnDesc))
+    lib.ssm_rmsnorm_fwd.argtypes = [norm] + [_vp] * 9
+    lib.ssm_rmsnorm_fwd.restype = ctypes.c_int
+    lib.ssm_rmsnorm_workspace_size.argtypes = [norm]
+    lib.ssm_rmsnorm_workspace_size.restype = ctypes.c_size_t
+    lib.ssm_rmsnorm_bwd.argtypes = [norm] + [_vp] * 8 + [ctypes.c_size_t, _vp]
+    lib.ssm_rmsnorm_bwd.restype = ctypes.c_int
+    lib.ssm_rope_frequencies.argtypes = ([ctypes.c_int64, ctypes.c_double, ctypes.c_int] +
+                                         [ctypes.c_double] * 4 +
+                                         [ctypes.POINTER(ctypes.c_double)])
+    lib.ssm_rope_frequencies.restype = ctypes.c_int
+    lib.ssm_rope_fwd.argtypes = [rope] + [_vp] * 7
+    lib.ssm_rope_fwd.restype = ctypes.c_int
+    lib.ssm_rope_bwd.argtypes = [rope] + [_vp] * 7
+    lib.ssm_rope_bwd.restype = ctypes.c_int
+    lib.ssm_linattn_workspace_size.argtypes = [la, ctypes.c_int]
+    lib.ssm_linattn_workspace_size.restype = ctypes.c_size_t
+    lib.ssm_linattn_fwd.argtypes = [la] + [_vp] * 9 + [ctypes.c_size_t, _vp]
+    lib.ssm_linattn_fwd.restype = ctypes.c_int
+    lib.ssm_linattn_bwd.argtypes = [la] + [_vp] * 13 + [ctypes.c_size_t, _vp]
+    lib.ssm_linattn_bwd.restype = ctypes.c_int
+    lib.ssm_linattn_step.argtypes = [la] + [_vp] * 7
+    lib.ssm_linattn_step.restype = ctypes.c_int
     lib.ssm_scan_last_error.argtypes = []
     lib.ssm_scan_last_error.restype = ctypes.c_char_p
     lib.ssm_scan_poll_device_error.argtypes = [_vp]
@@ -263,6 +327,78 @@ def ssm_preact_bwd(desc: Desc, z, dt_bias, lam_logit, ddt, dlam, dz, ddt_bias=No
     rc = lib.ssm_preact_bwd(ctypes.byref(desc), *[_ptr(t) for t in (
         z, dt_bias, lam_logit, ddt, dlam, dz, ddt_bias, dlam_logit)], _stream(stream))
     _check(rc, "ssm_preact_bwd")
+
+
+def ssm_rmsnorm_fwd(desc: RmsnormDesc, x, residual, weight, r, y, y8, scales, rstd,
+                    stream=None) -> None:
+    """r = x + residual; y = r rstd weight, and / or its e4m3 codes with scales."""
+    rc = load_library().ssm_rmsnorm_fwd(desc, _ptr(x), _ptr(residual), _ptr(weight), _ptr(r),
+                                        _ptr(y), _ptr(y8), _ptr(scales), _ptr(rstd),
+                                        _stream(stream))
+    _check(rc, "ssm_rmsnorm_fwd")
+
+
+def ssm_rmsnorm_workspace_size(desc: RmsnormDesc) -> int:
+    return load_library().ssm_rmsnorm_workspace_size(desc)
+
+
+def ssm_rmsnorm_bwd(desc: RmsnormDesc, dy, r, weight, rstd, dr, dx, dweight=None, workspace=None,
+                    workspace_bytes: int = 0, stream=None) -> None:
+    rc = load_library().ssm_rmsnorm_bwd(desc, _ptr(dy), _ptr(r), _ptr(weight), _ptr(rstd), _ptr(dr),
+                                        _ptr(dx), _ptr(dweight), _ptr(workspace), workspace_bytes,
+                                        _stream(stream))
+    _check(rc, "ssm_rmsnorm_bwd")
+
+
+def ssm_rope_frequencies(rot_dim: int, base: float, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+                         low_turns: float = 0.0, high_turns: float = 0.0,
+                         original_context: float = 0.0) -> list:
+    """The rot_dim / 2 frequencies (radians a position) of a base and a scaling."""
+    out = (ctypes.c_double * max(1, min(int(rot_dim), 1 << 16) // 2))()
+    _check(load_library().ssm_rope_frequencies(rot_dim, base, scaling, factor, low_turns,
+                                               high_turns, original_context, out),
+           "ssm_rope_frequencies")
+    return list(out)
+
+
+def ssm_rope_fwd(desc: RopeDesc, q, k, freq, positions, q_out, k_out, stream=None) -> None:
+    rc = load_library().ssm_rope_fwd(desc, _ptr(q), _ptr(k), _ptr(freq), _ptr(positions),
+                                     _ptr(q_out), _ptr(k_out), _stream(stream))
+    _check(rc, "ssm_rope_fwd")
+
+
+def ssm_rope_bwd(desc: RopeDesc, dq, dk, freq, positions, dq_out, dk_out, stream=None) -> None:
+    rc = load_library().ssm_rope_bwd(desc, _ptr(dq), _ptr(dk), _ptr(freq), _ptr(positions),
+                                     _ptr(dq_out), _ptr(dk_out), _stream(stream))
+    _check(rc, "ssm_rope_bwd")
+
+
+def ssm_linattn_workspace_size(desc: LinattnDesc, pass_: int) -> int:
+    return load_library().ssm_linattn_workspace_size(desc, pass_)
+
+
+def ssm_linattn_fwd(desc: LinattnDesc, q, k, v, log_decay, state_in, lengths, o, state_out=None,
+                    workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    rc = load_library().ssm_linattn_fwd(desc, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                        _ptr(state_in), _ptr(lengths), _ptr(o), _ptr(state_out),
+                                        _ptr(workspace), workspace_bytes, _stream(stream))
+    _check(rc, "ssm_linattn_fwd")
+
+
+def ssm_linattn_bwd(desc: LinattnDesc, q, k, v, log_decay, state_in, lengths, do, dstate_out, dq,
+                    dk, dv, dstate_in=None, workspace=None, workspace_bytes: int = 0,
+                    stream=None) -> None:
+    rc = load_library().ssm_linattn_bwd(desc, *[_ptr(t) for t in (
+        q, k, v, log_decay, state_in, lengths, do, dstate_out, dq, dk, dv, dstate_in, workspace)],
+        workspace_bytes, _stream(stream))
+    _check(rc, "ssm_linattn_bwd")
+
+
+def ssm_linattn_step(desc: LinattnDesc, q, k, v, log_decay, state, o, stream=None) -> None:
+    """One token; ``state`` (fp32) is updated in place."""
+    rc = load_library().ssm_linattn_step(desc, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                         _ptr(state), _ptr(o), _stream(stream))
+    _check(rc, "ssm_linattn_step")
 
 
 def ssm_scan_bwd(desc: Desc, x, dt, A_log, theta, B, C, D, lam, h0, prev_write, dy, dx, ddt,

@@ -450,6 +450,11 @@ int common_inputs(const ssm_desc_t *d, const void *x, const void *dt, const floa
 }  // namespace
 
 namespace ssm {
+// error state and timing hooks of the entry points outside this file
+int abi_fail(int code, const char *msg) { return fail(code, "%s", msg); }
+void abi_ok() { g_last_error.clear(); }
+void abi_profile_begin(cudaStream_t st) { profile_begin(st); }
+void abi_profile_end() { profile_end(); }
 void profile_mark(cudaStream_t st, const char *name) {
     if (!g_prof.active || g_prof.cur < 0 || g_prof.used >= g_prof.pool.size()) return;
     cudaEventRecord(g_prof.pool[g_prof.used], st);

@@ -1,0 +1,488 @@
+"""The layer operators on a GPU against their 64-bit forms (layer_ref.py).
+
+Bounds, per value, in units of what the arithmetic does:
+
+* a rounding to the I/O type: HALF[type] |ref|;
+* fp32 arithmetic: c 2^-24 times the sum of the magnitudes of the terms, c the roundings on
+  the longest path;
+* linear attention on tensor cores: scores and the entering state are rounded to bf16
+  once, half a step (2^-8) of each term's magnitude; states are carried with 24 bits.
+"""
+import numpy as np
+import pytest
+
+from selective_diagonal_state_b200 import abi
+from tests import layer_ref as R
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from selective_diagonal_state_b200 import build
+    build.build()
+    abi.load_library()
+
+
+@pytest.fixture(scope="module")
+def layer():
+    from selective_diagonal_state_b200 import layer
+    return layer
+
+
+def rounder(t):
+    return lambda a: torch.from_numpy(np.asarray(a)).to(torch.float32).to(DT[t]).double().numpy()
+
+
+def draw(g, shape, t, scale=1.0):
+    """(device tensor, its values in 64 bits)"""
+    x = torch.from_numpy(g.standard_normal(shape).astype(np.float32) * np.float32(scale)).to(DT[t])
+    return x.cuda(), x.double().numpy()
+
+
+def np64(x):
+    return x.detach().double().cpu().numpy()
+
+
+def close(name, got, ref, bound):
+    got = np64(got)
+    assert got.shape == ref.shape, name
+    # 2^-126: what is smaller than fp32's normal numbers may become 0
+    off = np.abs(got - ref) - np.broadcast_to(bound, ref.shape) - 2.0 ** -126
+    assert np.isfinite(got).all(), name
+    i = int(off.argmax()) if off.size else 0
+    assert off.size == 0 or off.flat[i] <= 0, (
+        f"{name}[{np.unravel_index(i, ref.shape)}]: {got.flat[i]!r} for {ref.flat[i]!r}, "
+        f"{off.flat[i]:.3g} above the bound")
+
+
+# ---- RMS norm --------------------------------------------------------------------------
+
+# a value: its product's three roundings, rsqrt's two, and the sum of squares, whose longest
+# chain is 32 values of a thread (or dim / 256 of one in the unaligned kernel) and 10 additions
+def norm_ops(dim):
+    return 5 + 0.5 * (max(32, dim / 256) + 10)
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,dim,res", [
+    (1, 1, False), (3, 7, True), (1, 8, True), (5, 64, True), (2, 128, False), (9, 256, True),
+    (33, 1000, True), (4, 1536, True), (7, 2048, False), (3, 4096, True), (2, 8192, True),
+    (2, 16384, True), (1, 20000, False), (300, 24, True)])
+def test_norm_and_gradient(layer, t, rows, dim, res):
+    g = np.random.default_rng(rows * 131 + dim)
+    x, xn = draw(g, (rows, dim), t)
+    rs, rn = draw(g, (rows, dim), t, 2.0) if res else (None, None)
+    w, wn = draw(g, (dim,), "fp32")
+    f = layer.rmsnorm(x, w, residual=rs, eps=1e-5, want_rstd=True)
+    r, y, rstd = R.norm(xn, rn, wn, float(np.float32(1e-5)), rounder(t))
+    c = norm_ops(dim) * R.U32
+    assert np.array_equal(np64(f.r), r)
+    close("rstd", f.rstd, rstd, c * rstd)
+    close("y", f.y, y, (R.HALF[t] + c) * np.abs(y))
+    dy, dyn = draw(g, (rows, dim), t)
+    dr, drn = draw(g, (rows, dim), t) if res else (None, None)
+    dx, dw = layer.rmsnorm_backward(dy, f.r, w, f.rstd, dr=dr)
+    rdx, rdw = R.norm_bwd(dyn, r, wn, rstd, drn)
+    xhat, up = np.abs(r * rstd[:, None]), np.abs(dyn * wn)
+    size = rstd[:, None] * (up + xhat * (xhat * up).mean(-1, keepdims=True)) + (0 if drn is None else np.abs(drn))
+    close("dx", dx, rdx, R.HALF[t] * np.abs(rdx) + 3 * c * size)
+    # dweight: rows / blocks sums in a thread, then at most 296 / 8 + 8 + 16
+    close("dweight", dw, rdw, (c + (rows + 61) * R.U32) * (np.abs(dyn) * xhat).sum(0))
+
+
+def test_norm_without_a_weight_and_shapes(layer):
+    g = np.random.default_rng(3)
+    x, xn = draw(g, (2, 3, 72), "bf16")
+    f = layer.rmsnorm(x, want_rstd=True)
+    assert f.r is x and f.rstd.shape == (2, 3)
+    _, y, _ = R.norm(xn, None, None, 1e-5, None)
+    close("y", f.y, y, (R.HALF["bf16"] + norm_ops(72) * R.U32) * np.abs(y))
+    dx, dw = layer.rmsnorm_backward(x, f.r, None, f.rstd)
+    assert dw is None and dx.shape == x.shape
+    last = layer.rmsnorm(x[:, 1:2])                 # one token of each sequence
+    assert torch.equal(last.y, f.y[:, 1:2])
+    with pytest.raises(ValueError, match="evenly"):
+        layer.rmsnorm(x[:, :2])
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("quant,rows,dim,off", [
+    ("row", 3, 100, 0), ("row", 5, 2048, 0), ("block", 4, 128, 0), ("block", 2, 2048, 0),
+    ("block", 9, 640, 0), ("row", 2, 16384, 0), ("block", 2, 20480, 0), ("row", 2, 20480, 0),
+    ("block", 3, 256, 1), ("row", 3, 256, 3)])
+def test_norm_codes(layer, t, quant, rows, dim, off):
+    """Codes and scales, with aligned rows and with rows that start `off` values in."""
+    g = np.random.default_rng(dim + rows)
+    x, _ = draw(g, (rows, dim + 2 * off), t)
+    x = x[:, off: off + dim]
+    xn = np64(x)
+    w, wn = draw(g, (dim,), "fp32")
+    f = layer.rmsnorm(x, w, quant=quant, want_y=True)
+    _, y, _ = R.norm(xn, None, wn, 1e-5, None)
+    c = norm_ops(dim) * R.U32
+    close("y", f.y, y, (R.HALF[t] + c) * np.abs(y))
+    width = 128 if quant == "block" else dim
+    top = np.abs(y).reshape(rows, -1, width).max(-1)
+    close("scales", f.scales, top / 448, (c + 2 * R.U32) * top / 448)
+    code = f.y8.float().double().cpu().numpy()
+    want = y / np.repeat(top / 448, width, 1)
+    # half a step of e4m3 (subnormal steps of 2^-9 below 2^-6), and the fp32 arithmetic before it
+    assert np.abs(code).max() <= 448
+    assert (np.abs(code - want) <= np.maximum(R.HALF["e4m3"] * np.abs(want), 2.0 ** -10) + (2 * c + 4 * R.U32) * np.abs(want)).all()
+
+
+def test_norm_codes_of_zeros_tiny_and_broken_rows(layer):
+    x = torch.zeros(4, 256, device="cuda")
+    x[1, 130] = 1e-30
+    x[2, 3] = float("inf")
+    x[3, 200] = float("nan")
+    for quant in ("row", "block"):
+        f = layer.rmsnorm(x, eps=1.0, quant=quant)
+        code = f.y8.float()
+        assert (code[0] == 0).all() and (f.scales[0] == 0).all()
+        assert code[1, 130] == 448 and (code[1, :130] == 0).all()
+        assert torch.isnan(code[3, 200])
+        assert not torch.isfinite(f.scales[3]).all() and not torch.isfinite((code[2] * 1.0)).all()
+
+
+def test_norm_in_place_and_broadcast(layer):
+    """The sum may overwrite x or the residual; a residual may be one row for all."""
+    g = np.random.default_rng(8)
+    x, xn = draw(g, (6, 512), "bf16")
+    one, on = draw(g, (1, 512), "bf16")
+    want = layer.rmsnorm(x, residual=one.expand(6, 512))
+    assert np.array_equal(np64(want.r), rounder("bf16")(xn + on))
+    x2, res = x.clone(), one.repeat(6, 1)
+    a = layer.rmsnorm(x2, residual=res, r=x2)
+    b = layer.rmsnorm(x, residual=res, r=res)
+    for f in (a, b):
+        assert torch.equal(f.r, want.r) and torch.equal(f.y, want.y)
+    dy, _ = draw(g, (6, 512), "bf16")
+    f = layer.rmsnorm(x, want_rstd=True)
+    w = torch.ones(512, device="cuda")
+    dx, dw = layer.rmsnorm_backward(dy, x, w, f.rstd)
+    dy2 = dy.clone()
+    dx2, dw2 = layer.rmsnorm_backward(dy2, x, w, f.rstd, dx=dy2)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+    e = layer.rmsnorm(x[:0], w, want_rstd=True)
+    dx, dw = layer.rmsnorm_backward(dy[:0], x[:0], w, e.rstd)
+    assert dx.shape == (0, 512) and (dw == 0).all()
+
+
+# ---- rotary positions ------------------------------------------------------------------
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+@pytest.mark.parametrize("B,L,hq,hk,dim,rot", [
+    (1, 1, 1, 1, 2, 2), (2, 3, 4, 2, 64, 64), (1, 70, 3, 1, 64, 32), (3, 5, 2, 2, 80, 20),
+    (2, 9, 5, 1, 96, 48), (1, 17, 24, 3, 128, 128), (2, 4, 1, 4, 33, 6), (1, 300, 2, 2, 256, 64)])
+def test_rope_and_gradient(layer, t, layout, B, L, hq, hk, dim, rot):
+    g = np.random.default_rng(dim * rot + L)
+    q, qn = draw(g, (B, L, hq, dim), t)
+    k, kn = draw(g, (B, L, hk, dim), t)
+    freq = layer.rope_frequencies(rot, scaling="linear", factor=2.0)
+    fn = np64(freq)
+    pos = torch.from_numpy(g.integers(-5, 1 << 20, (B, L))).cuda()
+    pos[0, 0] = (1 << 33) + 12345           # past 32 bits
+    pn = pos.cpu().numpy()
+    mag = 1.25
+    # sines: the angle's 64-bit error (2^-52 of 2^33 positions) and 2 ulp; a product, a sum
+    c = 8 * R.U32 + 2.0 ** -18 * R.U32 * 64
+    for sign, call in ((1.0, layer.rope), (-1.0, layer.rope_backward)):
+        oq, ok = call(q, k, freq, pos, layout=layout, magnitude=mag)
+        for name, got, xn in (("q", oq, qn), ("k", ok, kn)):
+            ref = R.rope(xn, fn, pn, layout, mag, sign)
+            size = R.rope(np.abs(xn), np.zeros(rot // 2), pn, layout, mag)
+            other = np.abs(xn)
+            part = other.copy()
+            m = rot // 2
+            if layout == "half":
+                part[..., :m], part[..., m:rot] = other[..., m:rot], other[..., :m]
+            else:
+                part[..., 0:rot:2], part[..., 1:rot:2] = other[..., 1:rot:2], other[..., 0:rot:2]
+            part[..., rot:] = 0
+            close(name, got, ref, R.HALF[t] * np.abs(ref) * (np.arange(dim) < rot) + c * (size + mag * part))
+    iq, ik = q.clone(), k.clone()
+    layer.rope(iq, ik, freq, pos, layout=layout, magnitude=mag, q_out=iq, k_out=ik)
+    wq, wk = layer.rope(q, k, freq, pos, layout=layout, magnitude=mag)
+    assert torch.equal(iq, wq) and torch.equal(ik, wk)
+    only, none = layer.rope(q, None, freq, pos, layout=layout, magnitude=mag)
+    assert torch.equal(only, wq) and none is None
+
+
+def test_rope_strides_and_default_positions(layer):
+    """q and k as views of one projection, [B, H, L, D] order, and positions 0, 1, ..."""
+    g = np.random.default_rng(5)
+    both, _ = draw(g, (2, 11, 6, 64), "bf16")
+    q, k = both[:, :, :4], both[:, :, 4:]
+    freq = layer.rope_frequencies(64)
+    a, b = layer.rope(q, k, freq)
+    pos = torch.arange(11, device="cuda")
+    c, d = layer.rope(q.contiguous(), k.contiguous(), freq, pos)
+    assert torch.equal(a, c) and torch.equal(b, d)
+    t = q.transpose(1, 2).contiguous().transpose(1, 2)
+    e, _ = layer.rope(t, None, freq, pos[None].expand(2, 11))
+    assert torch.equal(e, a)
+    odd = torch.zeros(2, 11, 4, 65, dtype=torch.bfloat16, device="cuda")[..., 1:]
+    odd.copy_(q)
+    f, _ = layer.rope(odd, None, freq)          # 2-byte aligned heads
+    assert (f.float() - a.float()).abs().max() <= 2.0 ** -7 * a.float().abs().max()
+    with pytest.raises(ValueError):
+        layer.rope(q, k, freq.float())
+    with pytest.raises(ValueError):
+        layer.rope(q, k, freq, pos.int())
+
+
+# ---- linear attention ------------------------------------------------------------------
+
+def la_case(seed, t, B, L, H, G, dk, dv, ragged, with_state=True, gmin=1e-3):
+    g = np.random.default_rng(seed)
+    T, N = {}, {}
+    for name, shape in (("q", (B, L, H, dk)), ("k", (B, L, G, dk)), ("v", (B, L, G, dv)), ("do", (B, L, H, dv))):
+        T[name], N[name] = draw(g, shape, t)
+    for name in ("state", "dstate"):
+        T[name], N[name] = draw(g, (B, H, dk, dv), "fp32") if with_state else (None, None)
+    dec = torch.from_numpy(-np.exp(g.uniform(np.log(gmin), 0.7, H)).astype(np.float32))
+    T["log_decay"], N["log_decay"] = dec.cuda(), dec.double().numpy()
+    T["lengths"] = N["lengths"] = None
+    if ragged:
+        n = g.integers(0, L + 1, B)
+        n[0] = 0 if B > 1 else n[0]
+        n[-1] = L
+        N["lengths"] = n
+        T["lengths"] = torch.from_numpy(n.astype(np.int32)).cuda()
+        for name in ("q", "k", "v", "do"):      # nothing behind a length may matter
+            for b in range(B):
+                T[name][b, n[b]:] = float("nan")
+    return T, N
+
+
+def la_bounds(N, scale, L, da):
+    """Sums of magnitudes of every output, and the fp32 roundings on the longest path."""
+    A = {k: (None if v is None else np.abs(v)) for k, v in N.items() if k not in ("log_decay", "lengths")}
+    o, S = R.linattn(A["q"], A["k"], A["v"], N["log_decay"], scale, A["state"], N["lengths"])
+    gr = R.linattn_bwd(A["q"], A["k"], A["v"], N["log_decay"], scale, A["do"], A["state"], A["dstate"], N["lengths"])
+    return o, S, gr
+
+
+def la_check(layer, T, N, t, scale, tensor, route=abi.LINATTN_AUTO):
+    B, L, H, dk = N["q"].shape
+    dv = N["v"].shape[3]
+    ob, sb, gb = la_bounds(N, scale, L, dk)
+    # a token's weight and sums: 3 roundings a token (recurrence) or 60 a chunk (tensor cores,
+    # 24 truncated accumulations of 2^-23 and the update), then the product over the head
+    c = ((60 * -(-L // 128) if tensor else 3 * L) + 2 * max(dk, dv) + 16) * R.U32
+    mid = R.HALF["bf16"] if tensor else 0.0
+    n = N["lengths"]
+    out = torch.full((B, L, H, dv), 7.0, dtype=DT[t], device="cuda")
+    o, S = layer.linattn(T["q"], T["k"], T["v"], T["log_decay"], scale=scale, state=T["state"],
+                         lengths=T["lengths"], out=out, route=route)
+    ro, rS = R.linattn(N["q"], N["k"], N["v"], N["log_decay"], scale, N["state"], n)
+    live = np.ones((B, L), bool) if n is None else np.arange(L)[None] < n[:, None]
+    hide = lambda x: np.where(live[..., None, None], x, 7.0)  # noqa: E731
+    close("o", o, hide(ro), (R.HALF[t] * np.abs(ro) + (mid + c) * ob) * live[..., None, None])
+    close("state", S, rS, c * sb)
+    grads = [torch.full_like(T[x], 7.0) for x in ("q", "k", "v")]
+    got = layer.linattn_backward(T["q"], T["k"], T["v"], T["log_decay"], T["do"], scale=scale, state=T["state"],
+                                 dstate=T["dstate"], lengths=T["lengths"], out=grads, route=route)
+    ref = R.linattn_bwd(N["q"], N["k"], N["v"], N["log_decay"], scale, N["do"], N["state"], N["dstate"], n)
+    for name, a, r, b in zip(("dq", "dk", "dv"), got, ref, gb):
+        close(name, a, hide(r), (R.HALF[t] * np.abs(r) + (mid + c) * b) * live[..., None, None])
+    close("dstate", got[3], ref[3], c * gb[3])
+    # the roundings are independent: in the 2-norm the errors stay below one bf16 half step
+    # for the stored value and one for the scores and the state
+    for name, a, r in [("o", o, hide(ro))] + [(x, a, hide(r)) for x, a, r in zip(("dq", "dk", "dv"), got, ref)]:
+        off = np.linalg.norm((np64(a) - r) * live[..., None, None])
+        assert off <= (2.0 ** 0.5 * R.HALF[t] + c) * np.linalg.norm(r * live[..., None, None]) + 1e-30, name
+
+
+RECURRENT = [
+    # t, B, L, H, G, dk, dv, ragged, state
+    ("fp32", 1, 1, 1, 1, 1, 1, False, False), ("fp32", 2, 19, 4, 2, 16, 24, True, True),
+    ("fp32", 1, 130, 2, 1, 65, 33, False, True), ("fp32", 3, 40, 2, 2, 128, 130, True, False),
+    ("bf16", 2, 37, 3, 3, 20, 12, True, True), ("bf16", 1, 21, 2, 1, 256, 200, False, True),
+    ("fp32", 2, 300, 4, 2, 16, 24, False, True)]
+
+
+@pytest.mark.parametrize("t,B,L,H,G,dk,dv,ragged,state", RECURRENT)
+def test_linattn_recurrent(layer, t, B, L, H, G, dk, dv, ragged, state):
+    T, N = la_case(L + dk, t, B, L, H, G, dk, dv, ragged, state)
+    la_check(layer, T, N, t, 0.37, False)
+
+
+CHUNKED = [
+    (1, 1, 1, 1, 64, 64, False, False), (1, 127, 2, 2, 64, 64, False, True), (1, 128, 2, 1, 128, 128, False, True),
+    (2, 129, 2, 2, 128, 64, False, False), (3, 200, 4, 2, 64, 128, True, True), (1, 257, 4, 4, 64, 64, False, True),
+    (4, 300, 6, 2, 128, 128, True, True), (2, 700, 2, 1, 72, 40, True, True), (1, 1000, 1, 1, 8, 8, False, True),
+    (1, 2300, 3, 1, 128, 128, False, True), (2, 1500, 1, 1, 96, 120, True, False)]
+
+
+@pytest.mark.parametrize("B,L,H,G,dk,dv,ragged,state", CHUNKED)
+def test_linattn_chunked(layer, B, L, H, G, dk, dv, ragged, state):
+    T, N = la_case(L * 3 + dk, "bf16", B, L, H, G, dk, dv, ragged, state)
+    la_check(layer, T, N, "bf16", dk ** -0.5, True)
+
+
+@pytest.mark.parametrize("t,dim", [("fp32", 24), ("bf16", 64)])
+def test_linattn_decays_at_the_ends(layer, t, dim):
+    """No decay at all, one that keeps nothing, and steep ones, in one call."""
+    T, N = la_case(4, t, 1, 260, 4, 4, dim, dim, False)
+    dec = torch.tensor([0.0, -float("inf"), -200.0, -30.0])
+    T["log_decay"], N["log_decay"] = dec.cuda(), np.array([0.0, -1e9, -200.0, -30.0])
+    la_check(layer, T, N, t, 0.2, t == "bf16")
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+def test_linattn_strides(layer, t):
+    """q, k and v as views of one projection, [B, H, L, D] order, odd offsets, and inputs
+    broadcast over the batch give what dense copies give."""
+    g = np.random.default_rng(2)
+    qkv, _ = draw(g, (2, 150, 4 + 2 + 2, 64), t)
+    views = qkv[:, :, :4], qkv[:, :, 4:6], qkv[:, :, 6:]
+    dec = torch.tensor([-0.01, -0.1, -0.5, -1.0], device="cuda")
+    do, _ = draw(g, (2, 150, 4, 64), t)
+    o, S = layer.linattn(*[x.contiguous() for x in views], dec)
+    back = layer.linattn_backward(*[x.contiguous() for x in views], dec, do)
+    for form in (lambda x: x, lambda x: x.transpose(1, 2).contiguous().transpose(1, 2)):
+        o2, S2 = layer.linattn(*map(form, views), dec, out=form(torch.zeros_like(o)))
+        assert torch.equal(o, o2) and torch.equal(S, S2)
+        b2 = layer.linattn_backward(*map(form, views), dec, form(do))
+        assert all(torch.equal(x, y) for x, y in zip(back, b2))
+    odd = [torch.zeros(*x.shape[:3], 65, dtype=x.dtype, device="cuda")[..., 1:] for x in views]
+    for x, y in zip(odd, views):
+        x.copy_(y)
+    o3, S3 = layer.linattn(*odd, dec)           # unaligned: the recurrence
+    lim = {"bf16": 4 * 2.0 ** -8, "fp32": 1e-5}[t]
+    assert (o3.float() - o.float()).norm() <= lim * o.float().norm() and (S3 - S).norm() <= 1e-5 * S.norm()
+    one = [x[:1].expand(2, -1, -1, -1) for x in views]
+    o4, S4 = layer.linattn(*one, dec)
+    o5, S5 = layer.linattn(*[x.contiguous() for x in one], dec)
+    assert torch.equal(o4, o5) and torch.equal(S4, S5)
+
+
+@pytest.mark.parametrize("t,B,H,G,dk,dv", [("bf16", 1, 1, 1, 64, 64), ("bf16", 5, 4, 2, 128, 64), ("fp32", 2, 3, 1, 33, 70),
+                                           ("bf16", 3, 2, 2, 256, 130), ("fp32", 2, 4, 4, 16, 24), ("bf16", 40, 16, 16, 128, 128)])
+def test_linattn_step(layer, t, B, H, G, dk, dv):
+    T, N = la_case(dk + dv, t, B, 3, H, G, dk, dv, False)
+    S = T["state"].clone()
+    ro, rS = R.linattn(N["q"], N["k"], N["v"], N["log_decay"], 0.3, N["state"])
+    ob, sb, _ = la_bounds(N, 0.3, 3, dk)
+    c = (3 * 6 + dk + 8) * R.U32
+    for i in range(3):
+        o = layer.linattn_step(*[T[x][:, i:i + 1] for x in ("q", "k", "v")], T["log_decay"], S, scale=0.3)
+        close("o", o, ro[:, i:i + 1], R.HALF[t] * np.abs(ro[:, i:i + 1]) + c * ob[:, i:i + 1])
+    close("state", S, rS, c * sb)
+
+
+def test_linattn_empty_and_in_place(layer):
+    g = np.random.default_rng(1)
+    S, _ = draw(g, (2, 4, 64, 64), "fp32")
+    dec = torch.full((4,), -0.1, device="cuda")
+    z = torch.zeros(2, 0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    o, S2 = layer.linattn(z, z, z, dec, state=S)
+    assert o.shape == z.shape and torch.equal(S, S2)
+    assert (layer.linattn(z, z, z, dec)[1] == 0).all()
+    assert torch.equal(layer.linattn_backward(z, z, z, dec, z, dstate=S)[3], S)
+    q, _ = draw(g, (2, 300, 4, 64), "bf16")
+    o1, S1 = layer.linattn(q, q, q, dec, state=S)
+    S3 = S.clone()
+    o2, _ = layer.linattn(q, q, q, dec, state=S3, state_out=S3)
+    assert torch.equal(o1, o2) and torch.equal(S1, S3)
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 3.0)
+    o4, S4 = layer.linattn(q, q, q, dec, state=S, lengths=zero, out=out)
+    assert (o4 == 3.0).all() and torch.equal(S4, S)
+    # lengths past the ends count as the ends
+    wild = torch.tensor([-5, 1 << 30], dtype=torch.int32, device="cuda")
+    o5, S5 = layer.linattn(q, q, q, dec, state=S, lengths=wild, out=out.clone())
+    assert (o5[0] == 3.0).all() and torch.equal(o5[1], o1[1]) and torch.equal(S5[0], S[0]) and torch.equal(S5[1], S1[1])
+
+
+# ---- together --------------------------------------------------------------------------
+
+def _block(layer, x, res, w, proj, freq, pos, dec, state=None, step=False):
+    """norm -> projection -> rotary positions -> linear attention, as one layer runs them."""
+    f = layer.rmsnorm(x, w, residual=res)
+    B, L = x.shape[:2]
+    qkv = (f.y @ proj).view(B, L, 4 + 2 + 2, 64)
+    q, k = layer.rope(qkv[:, :, :4], qkv[:, :, 4:6], freq, pos)
+    if step:
+        return layer.linattn_step(q, k, qkv[:, :, 6:], dec, state), state
+    return layer.linattn(q, k, qkv[:, :, 6:], dec, state=state)
+
+
+def test_prompt_then_steps_on_another_stream_and_in_a_graph(layer):
+    """The layer over a prompt and then one token at a time gives what the whole prompt gives;
+    the step captured into a graph and replayed too, and on a stream of its own."""
+    g = np.random.default_rng(9)
+    x, _ = draw(g, (2, 140, 256), "bf16")
+    res, _ = draw(g, (2, 140, 256), "bf16")
+    w, _ = draw(g, (256,), "fp32", 0.2)
+    proj, _ = draw(g, (256, 8 * 64), "bf16", 1 / 16)
+    freq = layer.rope_frequencies(64)
+    dec = torch.tensor([-0.02, -0.1, -0.4, -1.0], device="cuda")
+    pos = torch.arange(140, device="cuda")
+    whole, _ = _block(layer, x, res, w, proj, freq, pos, dec)
+    _, S = _block(layer, x[:, :137].contiguous(), res[:, :137].contiguous(), w, proj, freq, pos[:137], dec)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        o, _ = _block(layer, x[:, 137:138], res[:, 137:138], w, proj, freq, pos[137:138], dec, S, True)
+        xs, rs, ps = x[:, 138:139].clone(), res[:, 138:139].clone(), pos[138:139].clone()
+        keep = S.clone()
+        _block(layer, xs, rs, w, proj, freq, ps, dec, S, True)      # warm-up of the capture
+        S.copy_(keep)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        og, _ = _block(layer, xs, rs, w, proj, freq, ps, dec, S, True)
+    S.copy_(keep)
+    got = [o]
+    for i in (138, 139):
+        xs.copy_(x[:, i:i + 1])
+        rs.copy_(res[:, i:i + 1])
+        ps.copy_(pos[i:i + 1])
+        graph.replay()
+        got.append(og.clone())
+    got = torch.cat(got, 1).float()
+    want = whole[:, 137:].float()
+    # stored, scores and entering state rounded to bf16: as in la_check, on both sides
+    assert (got - want).norm() <= 2 * 2.0 ** 0.5 * 2.0 ** -8 * want.norm()
+
+
+def test_prompt_and_gradient_captured(layer):
+    """Forward and backward captured together and replayed on new inputs give what eager calls
+    give, bit by bit, while eager results of the same tensors live."""
+    T, _ = la_case(21, "bf16", 2, 270, 4, 2, 64, 64, False)
+    args = [T[x] for x in ("q", "k", "v", "log_decay")]
+    live = layer.linattn_backward(*args, T["do"], state=T["state"], dstate=T["dstate"])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        o = layer.linattn(*args, state=T["state"])
+        b = layer.linattn_backward(*args, T["do"], state=T["state"], dstate=T["dstate"])
+    for _ in range(2):
+        T["q"].neg_()
+        T["v"].mul_(0.5)
+        graph.replay()
+        eo = layer.linattn(*args, state=T["state"])
+        eb = layer.linattn_backward(*args, T["do"], state=T["state"], dstate=T["dstate"])
+        assert all(torch.equal(x, y) for x, y in zip(o + b, eo + eb))
+    assert all(torch.isfinite(x).all() for x in live)
+
+
+def test_calls_on_two_streams_at_once(layer):
+    T, _ = la_case(22, "bf16", 2, 400, 4, 4, 128, 64, False)
+    args = [T[x] for x in ("q", "k", "v", "log_decay")]
+    want = layer.linattn_backward(*args, T["do"])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [layer.linattn_backward(*args, T["do"], stream=s) for s in streams]
+    torch.cuda.synchronize()
+    for b in got:
+        assert all(torch.equal(x, y) for x, y in zip(b, want))
