@@ -40,6 +40,7 @@ size_t ssd_ring_bytes(long long B, long long H, long long L, int R);
 cudaError_t ssd_forward(const Params &p, cudaStream_t st);
 cudaError_t ssd_backward(const Params &p, cudaStream_t st);
 int ssd_error_take();
+int la_error_take();
 bool m1_supported(const Params &p);
 size_t m1_kept_floats(long long B, long long L, long long H, int N);
 size_t m1_part_floats(long long B, long long L, long long H, int N);
@@ -1007,6 +1008,8 @@ int ssm_scan_poll_device_error(void *stream) {
     if (word == 0 || word2 < 0) word = word2;
     const int word3 = ssm::ssd_error_take();
     if (word == 0 || word3 < 0) word = word3;
+    const int word4 = ssm::la_error_take();
+    if (word == 0 || word4 < 0) word = word4;
     if (word < 0) return fail(SSM_ERR_CUDA, "ssm_scan_poll_device_error: cannot read the error word");
     if (word == 1) return fail(SSM_ERR_TIMEOUT, "a bounded device-side wait gave up");
     if (word != 0) return fail(SSM_ERR_TIMEOUT, "device-side error code %d", word);

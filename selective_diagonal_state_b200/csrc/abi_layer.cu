@@ -236,18 +236,42 @@ LaArgs la_args(const ssm_linattn_desc_t *d, const float *log_decay, const int32_
     return p;
 }
 
-// workspace of the backward: per-head dk and dv where heads share a key and value head
-struct LaBwdWs {
-    size_t dk, dv, total;
+// Workspace of a call: per-head dk and dv of the backward where heads share a key and value
+// head, and the segment states of its walks on tensor cores.
+struct LaWs {
+    int nseg;   // 0: the recurrence
+    size_t dk, dv, seg[3], total;
 };
-LaBwdWs la_bwd_layout(const ssm_linattn_desc_t *d) {
-    LaBwdWs w = {};
-    if (d->nheads != d->nheads_kv) {
+LaWs la_layout(const ssm_linattn_desc_t *d, bool bwd) {
+    LaWs w = {};
+    const int ndk = (int)d->dim_k, ndv = (int)d->dim_v;
+    if (bwd && d->nheads != d->nheads_kv) {
         const size_t tok = (size_t)(d->batch * d->seqlen * d->nheads);
-        w.dv = align256(tok * d->dim_k * 4);
-        w.total = w.dv + align256(tok * d->dim_v * 4);
+        w.dv = align256(tok * ndk * 4);
+        w.total = w.dv + align256(tok * ndv * 4);
     }
+    if (d->route != SSM_LINATTN_AUTO) return w;
+    const bool bf16 = d->dtype_io == SSM_BF16;
+    if (!ssm::la_chunked_sizes(bf16, ndk, ndv) || (bwd && !ssm::la_chunked_sizes(bf16, ndv, ndk))) return w;
+    const int sk = (ndk + 63) / 64, sv = (ndv + 63) / 64;   // 64-column slices
+    w.nseg = ssm::la_segments(d->seqlen, d->batch * d->nheads * (bwd ? 2 * sk + sv : sv));
+    if (w.nseg > 1)
+        for (int i = 0; i < (bwd ? 3 : 1); ++i) {
+            w.seg[i] = w.total;
+            w.total += align256((size_t)w.nseg * (size_t)(d->batch * d->nheads * ndk * ndv) * 4);
+        }
     return w;
+}
+
+// the walks of `p` on tensor cores where they apply, else by the recurrence
+cudaError_t la_run(const LaArgs &p, const LaWs &ws, void *workspace, cudaStream_t st) {
+    if (ws.nseg) {
+        float *seg[3];
+        for (int i = 0; i < 3; ++i) seg[i] = (float *)((char *)workspace + ws.seg[i]);
+        cudaError_t e;
+        if (ssm::la_chunked(p, ws.nseg, seg, st, &e)) return e;
+    }
+    return ssm::la_recurrent(p, st);
 }
 
 int la_workspace(const char *where, size_t want, const void *ws, size_t bytes) {
@@ -364,7 +388,7 @@ int ssm_rope_bwd(const ssm_rope_desc_t *d, const void *dq, const void *dk, const
 
 size_t ssm_linattn_workspace_size(const ssm_linattn_desc_t *d, int pass) {
     if (check_la(d) != SSM_OK || d->batch == 0 || d->seqlen == 0) return 0;
-    return pass == SSM_PASS_BWD ? la_bwd_layout(d).total : 0;
+    return pass == SSM_PASS_BWD || pass == SSM_PASS_FWD ? la_layout(d, pass == SSM_PASS_BWD).total : 0;
 }
 
 int ssm_linattn_fwd(const ssm_linattn_desc_t *d, const void *q, const void *k, const void *v,
@@ -382,15 +406,15 @@ int ssm_linattn_fwd(const ssm_linattn_desc_t *d, const void *q, const void *k, c
         return launched("ssm_linattn_fwd (empty)", stream,
                         [&](cudaStream_t st) { return state_copy(state_out, state_in, d, st); });
     if ((rc = la_inputs(d, q, k, v, log_decay))) return rc;
-    if ((rc = la_workspace("ssm_linattn_fwd", ssm_linattn_workspace_size(d, SSM_PASS_FWD), workspace,
-                           workspace_bytes)))
-        return rc;
+    const LaWs ws = la_layout(d, false);
+    if ((rc = la_workspace("ssm_linattn_fwd", ws.total, workspace, workspace_bytes))) return rc;
     const int rep = (int)(d->nheads / d->nheads_kv), dk = (int)d->dim_k, dv = (int)d->dim_v;
     LaArgs p = la_args(d, log_decay, lengths);
     p.nwalk = 1;
     p.w[0] = walk({q, d->stride_q, 1, dk}, {k, d->stride_k, rep, dk}, {v, d->stride_v, rep, dv}, o,
                   d->stride_o, state_in, state_out, false, d->scale, 1.f, false);
-    return launched("ssm_linattn_fwd", stream, [&](cudaStream_t st) { return ssm::la_recurrent(p, st); });
+    return launched("ssm_linattn_fwd", stream,
+                    [&](cudaStream_t st) { return la_run(p, ws, workspace, st); });
 }
 
 int ssm_linattn_bwd(const ssm_linattn_desc_t *d, const void *q, const void *k, const void *v,
@@ -416,7 +440,7 @@ int ssm_linattn_bwd(const ssm_linattn_desc_t *d, const void *q, const void *k, c
     if ((rc = la_inputs(d, q, k, v, log_decay)) || (rc = need(do_, "do", es)) ||
         (rc = need(dq, "dq", es)) || (rc = need(dk, "dk", es)) || (rc = need(dv, "dv", es)))
         return rc;
-    const LaBwdWs ws = la_bwd_layout(d);
+    const LaWs ws = la_layout(d, true);
     if ((rc = la_workspace("ssm_linattn_bwd", ws.total, workspace, workspace_bytes))) return rc;
     const int rep = (int)(d->nheads / d->nheads_kv), ndk = (int)d->dim_k, ndv = (int)d->dim_v;
     const Operand oq = {q, d->stride_q, 1, ndk}, ok = {k, d->stride_k, rep, ndk},
@@ -434,7 +458,7 @@ int ssm_linattn_bwd(const ssm_linattn_desc_t *d, const void *q, const void *k, c
     p.w[2] = walk(ok, oq, odo, tv, shared ? hv : d->stride_dv, dstate_out, dstate_in, false, 1.f, d->scale, true);
     p.w[1].o_f32 = p.w[2].o_f32 = shared;
     return launched("ssm_linattn_bwd", stream, [&](cudaStream_t st) {
-        cudaError_t e = ssm::la_recurrent(p, st);
+        cudaError_t e = la_run(p, ws, workspace, st);
         if (e != cudaSuccess || !shared) return e;
         const long long sk[3] = {d->stride_dk[0], d->stride_dk[1], d->stride_dk[2]};
         const long long sv[3] = {d->stride_dv[0], d->stride_dv[1], d->stride_dv[2]};

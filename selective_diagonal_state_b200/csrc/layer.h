@@ -50,6 +50,11 @@ struct LaArgs {
     LaWalk w[3];
 };
 cudaError_t la_recurrent(const LaArgs &p, cudaStream_t st);
+// the walks on tensor cores (linattn_tc.cu)
+bool la_chunked_sizes(int bf16, int da, int dc);
+int la_segments(long long L, long long items);
+bool la_chunked(const LaArgs &p, int nseg, float *const *seg, cudaStream_t st, cudaError_t *err);
+int la_error_take();
 // sum of the `rep` heads that share a key / value head, fp32 [B][L][H][d] -> out
 cudaError_t la_group_sum(const float *in, void *out, const long long *so, int B, int L, int H,
                          int rep, int d, const int *lengths, int bf16, cudaStream_t st);
