@@ -8,18 +8,20 @@
 // four products with M = 128 on tcgen05: the scores A K^T, P V with the decayed, masked scores P
 // (bf16, in tensor memory), A S (S rounded to bf16) and K^T V'.  S itself stays in registers in
 // fp32.  Its update must not lose the 24 bits: V' = write lam^{n-1-j} v is split exactly into
-// three bf16 parts, each chunk's sum starts from zero in tensor memory (smallest parts first),
-// and is added to S in fp32.  P and the S of the readout are rounded to bf16 once, half a step
-// of 2^-8 on terms of an output that is itself stored as bf16.
+// three bf16 parts (truncations: 8 bits each), side by side as one operand of 192 columns so that
+// K is read once; each chunk's sums start from zero in tensor memory and are added to S in fp32.
+// P and the S of the readout are rounded to bf16 once, half a step of 2^-8 on terms of an output
+// that is itself stored as bf16.
 //
 // A block walks one segment of one (batch row, head), 64 columns of v and the state: per
-// chunk 80 KB come in by TMA and 16 KB go out.  One block an SM, its 16 warps with a role each:
-//     warp 0      TMA loads, two chunks ahead
-//     warp 1      all MMAs: the scores of chunk c + 1 before the other products of chunk c
-//     warps 4-7   P from the scores (a thread a token)
-//     warps 8-11  V', and the state (a thread a state row, 64 values in registers)
-//     warps 12-15 output (a thread a token)
-// so that loads, MMAs and the elementwise work of neighbouring chunks overlap.
+// chunk 80 KB come in by TMA and 16 KB go out.  One block an SM, its 20 warps with a role each:
+//     warp 0       TMA loads, two chunks ahead, each tile again as soon as its last reader is done
+//     warp 1       all MMAs, per chunk: A K^T, K^T V', A S, P V
+//     warps 4-11   P from the scores, and the output (a thread a token and half of the columns)
+//     warps 12-15  the state (a thread a state row, 64 values in registers)
+//     warps 16-19  V'
+// so that P is made while K^T V' and A S run, and V', the state and the output of one chunk
+// beside the products of the next.
 #include "chunk_common.cuh"
 #include "layer.h"
 
@@ -34,23 +36,27 @@ using namespace umma;
 using chunkc::WAIT_LIMIT;
 
 constexpr int C = 128;                   // tokens of a chunk
-constexpr int THREADS = 512;
+constexpr int THREADS = 640;
 constexpr uint32_t TILE = 16384;         // 128 rows x 128 bytes (64 bf16), 128-byte swizzle
 constexpr uint32_t ST_A = 0, ST_K = 2 * TILE, ST_V = 4 * TILE, STAGE = 5 * TILE;
 constexpr uint32_t SM_VP = 2 * STAGE;    // V' in three parts
 constexpr uint32_t SM_S = SM_VP + 3 * TILE;   // S as the bf16 operand of the readout
 constexpr uint32_t SM_F32 = SM_S + TILE;
 constexpr int F_PW = 0;                  // [129] lam^m
-constexpr int F_W = 132;                 // [256] read write lam^m at 128 + m, zero below
-constexpr int F_END = F_W + 256;
+constexpr int F_W = 132;                 // [160] read write lam^m at 32 + m, zero below
+constexpr int F_UP = F_W + 160;          // [32] lam^u
+constexpr int F_DOWN = F_UP + 32;        // [32] lam^{31 - u}
+constexpr int F_END = F_DOWN + 32;
 constexpr uint32_t SM_BAR = SM_F32 + F_END * 4;
-constexpr uint32_t SMEM_BYTES = SM_BAR + 160 + 1024;
+constexpr uint32_t SMEM_BYTES = SM_BAR + 224 + 1024;
+static_assert(F_UP % 4 == 0 && F_DOWN % 4 == 0, "16-byte rows");
 static_assert(SM_BAR % 8 == 0 && SMEM_BYTES <= 232448, "one block an SM");
 // tensor memory columns
-constexpr uint32_t TM_SC = 0;            // 2 x 128: scores, then P in their first 64 columns
-constexpr uint32_t TM_OI = 256;          // 64: P V
-constexpr uint32_t TM_OS = 320;          // 64: A S
-constexpr uint32_t TM_KV = 384;          // 64: K^T V'
+constexpr uint32_t TM_SC = 0;            // 128: scores
+constexpr uint32_t TM_OI = 128;          // 64: P V
+constexpr uint32_t TM_OS = 192;          // 64: A S
+constexpr uint32_t TM_KV = 256;          // 3 x 64: K^T V', a part each
+constexpr uint32_t TM_P = 448;           // 64: P, two bf16 a column
 constexpr uint32_t TM_COLS = 512;
 
 struct Maps {
@@ -58,11 +64,28 @@ struct Maps {
 };
 struct Args {
     LaArgs p;
+    int o32[3];      // the output takes 32-byte stores
     float *seg[3];   // [segment][b H + h][da][dc]: what a segment adds, then its entering state
     int nseg, G;     // segments of G chunks
     int slices;      // 64-column slices, the most of all walks
 };
 
+// Descriptor (umma.cuh, sdesc) of 128-byte-swizzled rows with leading offset LBO, at an address
+// in 16-byte units: only its low word is not constant.
+template <uint32_t LBO> __device__ __forceinline__ uint64_t desc(uint32_t units) {
+    constexpr uint32_t hi = (1024u >> 4) | 1u << 14 | LAYOUT_SW128 << 29;
+    return (uint64_t)hi << 32 | (units | (LBO >> 4) << 16);
+}
+// One lane of a converged warp, known to the compiler to be one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(one));
+    return one != 0;
+}
 // D[tmem] (+)= A[tmem] * B[smem]; issued by one thread.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                             uint32_t idesc, bool accumulate) {
@@ -91,6 +114,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&a)[16], uin
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&a)[16], uint32_t (&b)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;\n" : LA_IO16(a), LA_IO16(b)::"memory");
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld8(uint32_t (&r)[8], uint32_t (&q)[8], uint32_t (&t)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(q[0]), "+r"(q[1]), "+r"(q[2]), "+r"(q[3]), "+r"(q[4]), "+r"(q[5]), "+r"(q[6]), "+r"(q[7]),
+                   "+r"(t[0]), "+r"(t[1]), "+r"(t[2]), "+r"(t[3]), "+r"(t[4]), "+r"(t[5]), "+r"(t[6]), "+r"(t[7])
+                 :: "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -107,22 +142,55 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&r);
 }
+// the bf16 parts (high halves) of two floats as one word
+__device__ __forceinline__ uint32_t high2(float a, float b) {
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// (a.x b.x, a.y b.y) in one instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t &>(r))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return r;
+}
+__device__ __forceinline__ void st32(void *p, uint4 a, uint4 b) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
 
 struct Bars {
-    uint64_t full[2], empty[2], sc[2], p[2], vp, kv, s, o, ofree, end;
+    uint64_t a_full[2], k_full[2], v_full[2];   // tiles loaded
+    uint64_t a_free[2], k_free[2], v_free[2];   // tiles read by their last product
+    uint64_t sc, kv, o;                         // products done: scores; K^T V'; A S and P V
+    uint64_t p, vp, s;                          // operands written: P, V', S
+    uint64_t kv_read, o_read;                   // results fetched from tensor memory
+    uint64_t end;
     uint32_t tslot;
     int abort;
 };
-static_assert(sizeof(Bars) <= 160, "barrier space");
+static_assert(sizeof(Bars) <= 224, "barrier space");
 
 // Bounded wait for the completion number `n` (from 0) of a barrier; false, with the error word
-// and the block's abort flag raised, when it does not come or another role has given up.
+// and the block's abort flag raised, when it does not come or another role has given up.  The
+// hint lets the hardware keep the thread suspended: polls of 16 waiting warps would take the
+// issue slots that the others need.
+constexpr uint32_t POLL_NS = 20000, POLLS = 1u << 15;   // about half a second
 __device__ __forceinline__ bool await(Bars *B, uint64_t *bar, uint32_t n) {
-    for (uint32_t i = 0; i < WAIT_LIMIT; ++i) {
-        if (mbar_try_wait(bar, n & 1u)) return true;
-        if ((i & 63u) == 63u && *reinterpret_cast<volatile int *>(&B->abort)) return false;
+#pragma unroll 1
+    for (uint32_t i = 0; i < POLLS; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(n & 1u), "r"(POLL_NS)
+            : "memory");
+        if (ok) return true;
+        if (*reinterpret_cast<volatile int *>(&B->abort)) return false;
     }
     *reinterpret_cast<volatile int *>(&B->abort) = 1;
     atomicCAS(&ssm_la_error_word, 0, 1);
@@ -167,18 +235,12 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
     Bars *B = reinterpret_cast<Bars *>(sm + SM_BAR);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&B->full[i], 1);
-            mbar_init(&B->empty[i], 1);
-            mbar_init(&B->sc[i], 1);
-            mbar_init(&B->p[i], 4);
-        }
-        mbar_init(&B->vp, 4);
-        mbar_init(&B->kv, 1);
-        mbar_init(&B->s, 4);
-        mbar_init(&B->o, 1);
-        mbar_init(&B->ofree, 4);
-        mbar_init(&B->end, 1);
+        for (int i = 0; i < 2; ++i)
+            for (uint64_t *q : {&B->a_full[i], &B->k_full[i], &B->v_full[i], &B->a_free[i], &B->k_free[i], &B->v_free[i]})
+                mbar_init(q, 1);
+        for (uint64_t *q : {&B->sc, &B->kv, &B->o, &B->end}) mbar_init(q, 1);
+        for (uint64_t *q : {&B->vp, &B->s, &B->kv_read}) mbar_init(q, 4);    // an arrival a warp
+        for (uint64_t *q : {&B->p, &B->o_read}) mbar_init(q, 8);
         B->abort = 0;
         mbar_fence_init();
     }
@@ -186,10 +248,13 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
     {   // powers of lam from its logarithm in 64 bits: every one right to half a step
         double g = (double)p.log_decay[h];
         if (g < -1e6) g = -1e6;   // -inf: lam^0 stays 1
-        for (int i = tid; i < 129; i += THREADS) f32[F_PW + i] = (float)exp(g * i);
         const double rw = (double)w.read * (double)w.write;
-        for (int i = tid; i < 256; i += THREADS)
-            f32[F_W + i] = i < 128 ? 0.f : (float)(rw * exp(g * (i - 128)));
+        for (int i = tid; i < 129 + 160 + 64; i += THREADS) {
+            if (i < 129) f32[F_PW + i] = (float)exp(g * i);
+            else if (i < 289) f32[F_W + i - 129] = i < 161 ? 0.f : (float)(rw * exp(g * (i - 161)));
+            else if (i < 321) f32[F_UP + i - 289] = (float)exp(g * (i - 289));
+            else f32[F_DOWN + i - 321] = (float)exp(g * (352 - i));
+        }
     }
     fence_before_sync();
     __syncthreads();
@@ -200,148 +265,210 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
     // chunk number c of the walk: its first token and its tokens
     auto chunk = [&](int c) { return C * (first + (rev ? nch - 1 - c : c)); };
     auto ntok = [&](int t0) { return min(C, len - t0); };
-    const int nboxa = (w.da + 63) / 64;
+    // rows of the chunk's tiles that are other tokens (TMA fills those past L with zeros)
+    auto dirty = [&](int t0, int n) { return n < C && t0 + n < p.L; };
 
     if (warp == 0) {
         if (lane == 0) {
-            int c = 0;
-            for (; c < nch; ++c) {
-                const int s = c & 1;
-                if (c >= 2 && !await(B, &B->empty[s], (uint32_t)(c >> 1) - 1u)) break;
+            const int nboxa = (w.da + 63) / 64, ha = h / w.rep_a, hk = h / w.rep_k, hv = h / w.rep_v;
+            uint32_t got_a = 0, got_k = 0, got_v = 0;   // loads issued
+#pragma unroll 1
+            for (int c = 0; c < nch; ++c) {
+                const int s = c & 1, t0 = chunk(c);
+                const uint32_t n = (uint32_t)(c >> 1) - 1u;
                 unsigned char *st = sm + s * STAGE;
-                const int t0 = chunk(c);
-                mbar_expect_tx(&B->full[s], TILE * (3 + (STATE ? 0 : nboxa)));
-                tma_load_4d(st + ST_K, &maps->k, &B->full[s], 0, h / w.rep_k, t0, b);
-                if (!STATE)
-                    for (int i = 0; i < nboxa; ++i)
-                        tma_load_4d(st + ST_A + i * TILE, &maps->a, &B->full[s], 64 * i, h / w.rep_a, t0, b);
+                if (c >= 2 && !await(B, &B->k_free[s], n)) break;
+                mbar_expect_tx(&B->k_full[s], 2 * TILE);
+                tma_load_4d(st + ST_K, &maps->k, &B->k_full[s], 0, hk, t0, b);
                 // a second box past the head is zeros: state rows that are not there
-                tma_load_4d(st + ST_K + TILE, &maps->k, &B->full[s], 64, h / w.rep_k, t0, b);
-                tma_load_4d(st + ST_V, &maps->v, &B->full[s], c0, h / w.rep_v, t0, b);
+                tma_load_4d(st + ST_K + TILE, &maps->k, &B->k_full[s], 64, hk, t0, b);
+                ++got_k;
+                if (!STATE) {
+                    if (c >= 2 && !await(B, &B->a_free[s], n)) break;
+                    mbar_expect_tx(&B->a_full[s], TILE * nboxa);
+                    for (int i = 0; i < nboxa; ++i)
+                        tma_load_4d(st + ST_A + i * TILE, &maps->a, &B->a_full[s], 64 * i, ha, t0, b);
+                    ++got_a;
+                }
+                if (c >= 2 && !await(B, &B->v_free[s], n)) break;
+                mbar_expect_tx(&B->v_full[s], TILE);
+                tma_load_4d(st + ST_V, &maps->v, &B->v_full[s], c0, hv, t0, b);
+                ++got_v;
             }
             // no copy is in flight when the block ends
-            for (int i = max(0, c - 2); i < c; ++i) mbar_wait(&B->full[i & 1], (uint32_t)(i >> 1) & 1u, WAIT_LIMIT);
+            for (uint32_t i = 0; i < 2; ++i) {
+                if (got_a > i) mbar_wait(&B->a_full[(got_a - 1 - i) & 1], ((got_a - 1 - i) >> 1) & 1u, WAIT_LIMIT);
+                if (got_k > i) mbar_wait(&B->k_full[(got_k - 1 - i) & 1], ((got_k - 1 - i) >> 1) & 1u, WAIT_LIMIT);
+                if (got_v > i) mbar_wait(&B->v_full[(got_v - 1 - i) & 1], ((got_v - 1 - i) >> 1) & 1u, WAIT_LIMIT);
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t base = smem_u32(sm);
-            const uint32_t id_sc = idesc_bf16(128, 128, false, false), id_as = idesc_bf16(128, 64, false, true);
-            const uint32_t id_kv = idesc_bf16(128, 64, true, true);
+            constexpr uint32_t id_sc = idesc_bf16(128, 128, false, false), id_n = idesc_bf16(128, 64, false, true);
+            constexpr uint32_t id_kv = idesc_bf16(128, 192, true, true);
+            // descriptors: their address field counts 16-byte units; along a row, 16 values are 2 of them
+            const uint32_t u0 = base >> 4;
+            auto kmaj = [&](uint32_t tile, int s) { return desc<16u>(u0 + (tile >> 4) + (s >> 2) * (TILE >> 4) + (s & 3) * 2u); };
+            auto mnmaj = [&](uint32_t tile, int s) { return desc<TILE>(u0 + (tile >> 4) + 128u * s); };
             const int ks = (w.da + 15) / 16;
-            auto scores = [&](int c) {
-                const uint32_t st = base + (c & 1) * STAGE;
-                for (int s = 0; s < ks; ++s) {
-                    const uint32_t off = (uint32_t)(s >> 2) * TILE + (uint32_t)(s & 3) * 32u;
-                    mma_bf16(tm + TM_SC + 128u * (c & 1), sdesc(st + ST_A + off, 16u, 1024u, LAYOUT_SW128),
-                             sdesc(st + ST_K + off, 16u, 1024u, LAYOUT_SW128), id_sc, s > 0);
-                }
-                mma_commit(&B->sc[c & 1]);
-            };
-            auto kv = [&](int c) {   // the smallest part of V' first
-                const uint32_t st = base + (c & 1) * STAGE;
-                for (int q = 2; q >= 0; --q)
-                    for (int s = 0; s < C / 16; ++s)
-                        mma_bf16(tm + TM_KV, sdesc(st + ST_K + s * 2048u, TILE, 1024u, LAYOUT_SW128),
-                                 sdesc(base + SM_VP + q * TILE + s * 2048u, TILE, 1024u, LAYOUT_SW128), id_kv,
-                                 q < 2 || s > 0);
-                mma_commit(&B->kv);
-            };
-            bool ok = true;
-            if (!STATE && nch > 0) {
-                ok = await(B, &B->full[0], 0u);
-                if (ok) scores(0);
-            }
-            for (int c = 0; ok && c < nch; ++c) {
-                const uint32_t st = base + (c & 1) * STAGE;
+#pragma unroll 1
+            for (int c = 0; c < nch; ++c) {
+                const uint32_t st = (c & 1) ? STAGE : 0u;
+                const uint32_t half = (uint32_t)c >> 1;
+                if (!await(B, &B->k_full[c & 1], half)) break;
                 if (!STATE) {
-                    if (c + 1 < nch) {
-                        if (!(ok = await(B, &B->full[(c + 1) & 1], (uint32_t)(c + 1) >> 1))) break;
-                        scores(c + 1);
-                    }
+                    if (!await(B, &B->a_full[c & 1], half)) break;
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        if (s < ks) mma_bf16(tm + TM_SC, kmaj(st + ST_A, s), kmaj(st + ST_K, s), id_sc, s > 0);
+                    mma_commit(&B->sc);
                 }
-                if (!(ok = await(B, &B->s, (uint32_t)c))) break;   // S of this chunk, K^T V' free
-                if (!STATE) {
-                    if (c > 0 && !(ok = await(B, &B->ofree, (uint32_t)c - 1u))) break;
-                    fence_after_sync();
-                    for (int s = 0; s < ks; ++s)
-                        mma_bf16(tm + TM_OS,
-                                 sdesc(st + ST_A + (uint32_t)(s >> 2) * TILE + (uint32_t)(s & 3) * 32u, 16u, 1024u, LAYOUT_SW128),
-                                 sdesc(base + SM_S + s * 2048u, TILE, 1024u, LAYOUT_SW128), id_as, s > 0);
-                }
-                if (!(ok = await(B, &B->vp, (uint32_t)c))) break;
+                if (!await(B, &B->vp, (uint32_t)c)) break;
+                if (c > 0 && !await(B, &B->kv_read, (uint32_t)c - 1u)) break;
                 fence_after_sync();
-                kv(c);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    mma_bf16(tm + TM_KV, mnmaj(st + ST_K, s), mnmaj(SM_VP, s), id_kv, s > 0);
+                mma_commit(&B->kv);
+                mma_commit(&B->k_free[c & 1]);
                 if (!STATE) {
-                    if (!(ok = await(B, &B->p[c & 1], (uint32_t)c >> 1))) break;
+                    if (!await(B, &B->s, (uint32_t)c)) break;
+                    if (c > 0 && !await(B, &B->o_read, (uint32_t)c - 1u)) break;
                     fence_after_sync();
-                    for (int s = 0; s < C / 16; ++s)
-                        mma_bf16_ts(tm + TM_OI, tm + TM_SC + 128u * (c & 1) + 8u * s,
-                                    sdesc(st + ST_V + s * 2048u, TILE, 1024u, LAYOUT_SW128), id_as, s > 0);
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        if (s < ks) mma_bf16(tm + TM_OS, kmaj(st + ST_A, s), mnmaj(SM_S, s), id_n, s > 0);
+                    mma_commit(&B->a_free[c & 1]);
+                    if (!await(B, &B->p, (uint32_t)c)) break;
+                    fence_after_sync();
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        mma_bf16_ts(tm + TM_OI, tm + TM_P + 8u * s, mnmaj(st + ST_V, s), id_n, s > 0);
                     mma_commit(&B->o);
                 }
-                mma_commit(&B->empty[c & 1]);
+                mma_commit(&B->v_free[c & 1]);
             }
             mma_commit(&B->end);   // every MMA is over before tensor memory goes
             mbar_wait(&B->end, 0u, WAIT_LIMIT);
         }
         __syncwarp();
-    } else if (!STATE && warp >= 4 && warp < 8) {
-        // P[i][j] = read write lam^{|i - j|} (a_i . k_j) on one side of the diagonal
-        for (int c = 0; c < nch; ++c) {
-            if (!await_warp(B, &B->sc[c & 1], (uint32_t)c >> 1)) break;
-            fence_after_sync();
-            const int n = ntok(chunk(c)), qd = warp & 3;
-            const uint32_t t_sc = tm + TM_SC + 128u * (c & 1) + lane_q;
-            const float *wt = f32 + F_W + 128;
+    } else if (!STATE && warp >= 4 && warp < 12) {
+        const int half = (warp - 4) >> 2, qd = warp & 3;
+        const long long ob = b * w.so[0] + h * w.so[2] + c0 + 32 * half;
+        const int nq = min(4, (w.dc - c0 - 32 * half) / 8);   // 8-column pieces of the output (<= 0: none)
+        const bool wide = A.o32[wi] && nq == 4;
 #pragma unroll 1
-            for (int jb = 0; jb < 4; ++jb) {
+        for (int c = 0; c < nch; ++c) {
+            const int t0 = chunk(c), n = ntok(t0);
+            if (!await_warp(B, &B->sc, (uint32_t)c)) break;
+            fence_after_sync();
+            // P[i][j] = read write lam^{|i - j|} (a_i . k_j) on one side of the diagonal, 32 columns
+            // at a time
+#pragma unroll 1
+            for (int z = 0; z < 2; ++z) {
+                const int jb = 2 * half + z;
                 uint32_t o[16];
                 if (rev ? jb < qd : jb > qd) {   // masked
 #pragma unroll
                     for (int u = 0; u < 16; ++u) o[u] = 0u;
                 } else {
                     uint32_t x[16], y[16];
-                    tmem_ld32(t_sc + 32u * jb, x, y);
-                    const float *wr = rev ? wt + (32 * jb - row) : wt + (row - 32 * jb);
-                    const int d = rev ? 1 : -1;
-                    tmem_wait_ld(x, y);
-                    if (n == C) {
+                    tmem_ld32(tm + TM_SC + lane_q + 32u * jb, x, y);
+                    const int left = n - 32 * jb;   // columns of this sequence
+                    if (jb == qd || left < 32) {
+                        // the diagonal, and the sequence's end: tokens past it are not read, whatever they hold
+                        const int at = rev ? 32 * jb - row : row - 32 * jb, d = rev ? 1 : -1;
+                        float wv[32];
+#pragma unroll
+                        for (int u = 0; u < 32; ++u) wv[u] = f32[F_W + 32 + at + d * u];
+                        tmem_wait_ld(x, y);
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
-                            o[u] = pack2(__uint_as_float(x[2 * u]) * wr[d * (2 * u)],
-                                         __uint_as_float(x[2 * u + 1]) * wr[d * (2 * u + 1)]);
-                            o[8 + u] = pack2(__uint_as_float(y[2 * u]) * wr[d * (16 + 2 * u)],
-                                             __uint_as_float(y[2 * u + 1]) * wr[d * (17 + 2 * u)]);
+                            o[u] = pack2(2 * u < left ? __uint_as_float(x[2 * u]) * wv[2 * u] : 0.f,
+                                         2 * u + 1 < left ? __uint_as_float(x[2 * u + 1]) * wv[2 * u + 1] : 0.f);
+                            o[8 + u] = pack2(16 + 2 * u < left ? __uint_as_float(y[2 * u]) * wv[16 + 2 * u] : 0.f,
+                                             17 + 2 * u < left ? __uint_as_float(y[2 * u + 1]) * wv[17 + 2 * u] : 0.f);
                         }
-                    } else {   // tokens past the sequence are not read, whatever they hold
-                        const int left = n - 32 * jb;
+                    } else {
+                        // off it the weight is a factor of the row times one of the column
+                        const float r = f32[F_W + 32 + (rev ? 32 * jb - row : row - 32 * jb - 31)];
+                        const float4 *cw = reinterpret_cast<const float4 *>(f32 + (rev ? F_UP : F_DOWN));
+                        const float2 rr = make_float2(r, r);
+                        tmem_wait_ld(x, y);
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
-                            o[u] = pack2(2 * u < left ? __uint_as_float(x[2 * u]) * wr[d * (2 * u)] : 0.f,
-                                         2 * u + 1 < left ? __uint_as_float(x[2 * u + 1]) * wr[d * (2 * u + 1)] : 0.f);
-                            o[8 + u] = pack2(16 + 2 * u < left ? __uint_as_float(y[2 * u]) * wr[d * (16 + 2 * u)] : 0.f,
-                                             17 + 2 * u < left ? __uint_as_float(y[2 * u + 1]) * wr[d * (17 + 2 * u)] : 0.f);
+                            const float4 f = cw[u];
+                            const uint32_t *s4 = u < 4 ? x + 4 * u : y + 4 * (u - 4);
+                            const float2 e0 = mul2(mul2(make_float2(__uint_as_float(s4[0]), __uint_as_float(s4[1])), rr), make_float2(f.x, f.y));
+                            const float2 e1 = mul2(mul2(make_float2(__uint_as_float(s4[2]), __uint_as_float(s4[3])), rr), make_float2(f.z, f.w));
+                            o[2 * u] = pack2(e0.x, e0.y);
+                            o[2 * u + 1] = pack2(e1.x, e1.y);
                         }
                     }
                 }
-                tmem_st16(t_sc + 16u * jb, o);   // over scores that are in registers by now
+                tmem_st16(tm + TM_P + lane_q + 16u * jb, o);
             }
             tmem_wait_st();
             fence_before_sync();
-            warp_arrive(&B->p[c & 1]);
+            warp_arrive(&B->p);
+            if (!await_warp(B, &B->o, (uint32_t)c)) break;
+            fence_after_sync();
+            uint32_t x[16], y[16], u[16], v[16];
+            tmem_ld32(tm + TM_OI + lane_q + 32u * half, x, y);
+            tmem_ld32(tm + TM_OS + lane_q + 32u * half, u, v);
+            const float e = w.read * f32[F_PW + max(0, rev ? n - 1 - row : row + 1)];
+            tmem_wait_ld(x, y);
+            tmem_wait_ld(u, v);
+            fence_before_sync();
+            warp_arrive(&B->o_read);
+            float o[32];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                o[j] = fmaf(e, __uint_as_float(u[j]), __uint_as_float(x[j]));
+                o[16 + j] = fmaf(e, __uint_as_float(v[j]), __uint_as_float(y[j]));
+            }
+            if (row < n) {
+                const long long at = ob + (long long)(t0 + row) * w.so[1];
+                if (w.o_f32) {
+                    float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(w.o) + at);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (q < 2 * nq) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(w.o) + at);
+                    uint4 r[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        r[q] = make_uint4(pack2(o[8 * q], o[8 * q + 1]), pack2(o[8 * q + 2], o[8 * q + 3]),
+                                          pack2(o[8 * q + 4], o[8 * q + 5]), pack2(o[8 * q + 6], o[8 * q + 7]));
+                    if (wide) {
+                        st32(dst, r[0], r[1]);
+                        st32(dst + 2, r[2], r[3]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (q < nq) dst[q] = r[q];
+                    }
+                }
+            }
         }
-    } else if (warp >= 8 && warp < 12) {
+    } else if (warp >= 12 && warp < 16) {
         float S[64];
-        const int t = tid - 256;
         const bool live = row < w.da;
         const float *src = STATE && A.nseg > 1 ? nullptr   // a segment's own sum
                          : A.nseg > 1 ? A.seg[wi] + ((long long)sg * BH + bh) * w.da * w.dc
                          : w.s_in ? w.s_in + (long long)bh * w.da * w.dc : nullptr;
         const int sta = A.nseg > 1 ? w.dc : w.st_a, stc = A.nseg > 1 ? 1 : w.st_c;
+        const long long at = (long long)row * sta + (long long)c0 * stc;
+        const int cols = live ? w.dc - c0 : 0;
+        {
+            const float *q = src + at;
+            const int n = src ? cols : 0;
 #pragma unroll
-        for (int j = 0; j < 64; ++j)
-            S[j] = src && live && c0 + j < w.dc ? src[(long long)row * sta + (long long)(c0 + j) * stc] : 0.f;
+            for (int j = 0; j < 64; ++j, q += stc) S[j] = j < n ? *q : 0.f;
+        }
         auto operand = [&]() {   // S in bf16, the layout of a V tile
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -349,28 +476,66 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
                                            pack2(S[8 * q + 4], S[8 * q + 5]), pack2(S[8 * q + 6], S[8 * q + 7]));
                 *reinterpret_cast<uint4 *>(sm + SM_S + row * 128 + ((q ^ (row & 7)) << 4)) = v;
             }
+            fence_proxy_async();
+            warp_arrive(&B->s);
         };
         if (!STATE) operand();
-        fence_proxy_async();
-        warp_arrive(&B->s);
+#pragma unroll 1
+        for (int c = 0; c < nch; ++c) {
+            const float E = f32[F_PW + ntok(chunk(c))];
+            if (!await_warp(B, &B->kv, (uint32_t)c)) break;
+            fence_after_sync();
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                uint32_t x[8], y[8], z[8];
+                tmem_ld8(tm + TM_KV + lane_q + 8u * q, x);
+                tmem_ld8(tm + TM_KV + lane_q + 64u + 8u * q, y);
+                tmem_ld8(tm + TM_KV + lane_q + 128u + 8u * q, z);
+                tmem_wait_ld8(x, y, z);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    S[8 * q + j] = fmaf(E, S[8 * q + j],
+                                        __uint_as_float(x[j]) + (__uint_as_float(y[j]) + __uint_as_float(z[j])));
+            }
+            fence_before_sync();
+            warp_arrive(&B->kv_read);
+            if (!STATE && c + 1 < nch) {
+                // A S of this chunk has read the operand
+                if (!await_warp(B, &B->a_free[c & 1], (uint32_t)c >> 1)) break;
+                operand();
+            }
+        }
+        float *dst = A.nseg > 1 ? (STATE ? A.seg[wi] + ((long long)sg * BH + bh) * w.da * w.dc : nullptr)
+                                : w.s_out ? w.s_out + (long long)bh * w.da * w.dc : nullptr;
+        if (dst) {
+            float *q = dst + at;
+#pragma unroll
+            for (int j = 0; j < 64; ++j, q += stc)
+                if (j < cols) *q = S[j];
+        }
+    } else if (warp >= 16) {
+        const int t = tid - 512;
+#pragma unroll 1
         for (int c = 0; c < nch; ++c) {
             unsigned char *st = sm + (c & 1) * STAGE;
             const int t0 = chunk(c), n = ntok(t0);
-            if (!await_warp(B, &B->full[c & 1], (uint32_t)c >> 1)) break;
-            const bool dirty = n < C && t0 + n < p.L;   // rows of other tokens (TMA fills those past L with zeros)
-            if (dirty && !STATE && !await_warp(B, &B->sc[c & 1], (uint32_t)c >> 1)) break;   // the scores have read K
-#pragma unroll 2
+            const bool fix = dirty(t0, n);
+            if (!await_warp(B, &B->v_full[c & 1], (uint32_t)c >> 1)) break;
+            if (c > 0 && !await_warp(B, &B->kv, (uint32_t)c - 1u)) break;   // V' has been read
+            if (fix && !await_warp(B, &B->k_full[c & 1], (uint32_t)c >> 1)) break;
+            if (fix && !STATE && !await_warp(B, &B->sc, (uint32_t)c)) break;   // the scores have read K
+#pragma unroll 1
             for (int q = 0; q < 8; ++q) {
                 const int ch = t + 128 * q, r = ch >> 3;   // 16-byte piece of row r
                 const uint32_t off = (uint32_t)ch * 16u;
                 uint4 x = *reinterpret_cast<const uint4 *>(st + ST_V + off);
-                if (dirty && r >= n) {
+                if (fix && r >= n) {
                     x = make_uint4(0u, 0u, 0u, 0u);
                     *reinterpret_cast<uint4 *>(st + ST_V + off) = x;
                     *reinterpret_cast<uint4 *>(st + ST_K + off) = x;
                     *reinterpret_cast<uint4 *>(st + ST_K + TILE + off) = x;
                 }
-                const float f = r < n ? w.write * f32[F_PW + (rev ? r + 1 : n - 1 - r)] : 0.f;
+                const float f = w.write * f32[F_PW + (rev ? r + 1 : max(0, n - 1 - r))];
                 const uint32_t u[4] = {x.x, x.y, x.z, x.w};
                 uint32_t o[3][4];
 #pragma unroll
@@ -378,9 +543,9 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
                     float a = lo_f(u[i]) * f, bb = hi_f(u[i]) * f;
 #pragma unroll
                     for (int z = 0; z < 3; ++z) {
-                        o[z][i] = pack2(a, bb);
-                        a -= lo_f(o[z][i]);
-                        bb -= hi_f(o[z][i]);
+                        o[z][i] = high2(a, bb);
+                        a -= hi_f(__float_as_uint(a));
+                        bb -= hi_f(__float_as_uint(bb));
                     }
                 }
 #pragma unroll
@@ -389,71 +554,6 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
             }
             fence_proxy_async();
             warp_arrive(&B->vp);
-            if (!await_warp(B, &B->kv, (uint32_t)c)) break;
-            fence_after_sync();
-            const float E = f32[F_PW + n];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t x[16], y[16];
-                tmem_ld32(tm + TM_KV + lane_q + 32u * q, x, y);
-                tmem_wait_ld(x, y);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    S[32 * q + j] = fmaf(E, S[32 * q + j], __uint_as_float(x[j]));
-                    S[32 * q + 16 + j] = fmaf(E, S[32 * q + 16 + j], __uint_as_float(y[j]));
-                }
-            }
-            if (!STATE && c + 1 < nch) operand();   // A S of this chunk is over, as K^T V' is
-            fence_proxy_async();
-            fence_before_sync();
-            warp_arrive(&B->s);
-        }
-        float *dst = A.nseg > 1 ? (STATE ? A.seg[wi] + ((long long)sg * BH + bh) * w.da * w.dc : nullptr)
-                                : w.s_out ? w.s_out + (long long)bh * w.da * w.dc : nullptr;
-        if (dst && live)
-#pragma unroll
-            for (int j = 0; j < 64; ++j)
-                if (c0 + j < w.dc) dst[(long long)row * sta + (long long)(c0 + j) * stc] = S[j];
-    } else if (!STATE && warp >= 12) {
-        const long long ob = b * w.so[0] + h * w.so[2] + c0;
-        const int nq = min(8, (w.dc - c0) / 8);
-        for (int c = 0; c < nch; ++c) {
-            if (!await_warp(B, &B->o, (uint32_t)c)) break;
-            fence_after_sync();
-            const int t0 = chunk(c), n = ntok(t0);
-            const float e = w.read * f32[F_PW + max(0, rev ? n - 1 - row : row + 1)];
-            float o[64];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t x[16], y[16], u[16], v[16];
-                tmem_ld32(tm + TM_OI + lane_q + 32u * q, x, y);
-                tmem_ld32(tm + TM_OS + lane_q + 32u * q, u, v);
-                tmem_wait_ld(x, y);
-                tmem_wait_ld(u, v);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    o[32 * q + j] = fmaf(e, __uint_as_float(u[j]), __uint_as_float(x[j]));
-                    o[32 * q + 16 + j] = fmaf(e, __uint_as_float(v[j]), __uint_as_float(y[j]));
-                }
-            }
-            fence_before_sync();
-            warp_arrive(&B->ofree);
-            if (row < n) {
-                const long long at = ob + (long long)(t0 + row) * w.so[1];
-                if (w.o_f32) {
-                    float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(w.o) + at);
-#pragma unroll
-                    for (int q = 0; q < 16; ++q)
-                        if (q < 2 * nq) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-                } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(w.o) + at);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (q < nq)
-                            dst[q] = make_uint4(pack2(o[8 * q], o[8 * q + 1]), pack2(o[8 * q + 2], o[8 * q + 3]),
-                                                pack2(o[8 * q + 4], o[8 * q + 5]), pack2(o[8 * q + 6], o[8 * q + 7]));
-                }
-            }
         }
     }
     fence_before_sync();
@@ -547,6 +647,7 @@ bool la_chunked(const LaArgs &p, int nseg, float *const *seg, cudaStream_t st, c
         const int sl = (w.dc + 63) / 64;
         A.slices = sl > A.slices ? sl : A.slices;
         A.seg[i] = seg[i];
+        A.o32[i] = w.o && !w.o_f32 && ((uintptr_t)w.o & 31) == 0 && w.so[0] % 16 == 0 && w.so[1] % 16 == 0 && w.so[2] % 16 == 0;
     }
     const int nc = (p.L + C - 1) / C;
     A.G = (nc + nseg - 1) / nseg;
