@@ -22,6 +22,8 @@
 //     warps 16-19  V'
 // so that P is made while K^T V' and A S run, and V', the state and the output of one chunk
 // beside the products of the next.
+#include <atomic>
+
 #include "chunk_common.cuh"
 #include "layer.h"
 
@@ -601,6 +603,19 @@ bool make_map(CUtensorMap *m, const void *base, int d, int heads, const LaArgs &
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Allows the walks their shared memory, once a device.
+cudaError_t set_smem() {
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
+    if ((e = cudaFuncSetAttribute(k_la_walk<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) ||
+        (e = cudaFuncSetAttribute(k_la_walk<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)))
+        return e;
+    if (dev < 64) done.fetch_or(1ull << dev);
+    return cudaSuccess;
+}
+
 }  // namespace la
 
 // Walks that may take the tensor cores by their sizes.
@@ -654,12 +669,7 @@ bool la_chunked(const LaArgs &p, int nseg, float *const *seg, cudaStream_t st, c
     A.nseg = (nc + A.G - 1) / A.G;
     const bool state_only = p.nwalk == 1 && !p.w[0].o;
     const long long items = (long long)p.nwalk * A.nseg * p.B * p.H * A.slices;
-    cudaError_t e;
-    if ((e = cudaFuncSetAttribute(k_la_walk<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) ||
-        (e = cudaFuncSetAttribute(k_la_walk<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES))) {
-        *err = e;
-        return true;
-    }
+    if ((*err = set_smem()) != cudaSuccess) return true;
     if (A.nseg > 1 || state_only) {
         k_la_walk<true><<<(unsigned)items, THREADS, SMEM_BYTES, st>>>(m[0], m[1], m[2], A);
         profile_mark(st, "k_la_walk_state");

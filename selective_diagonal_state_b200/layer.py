@@ -2,15 +2,20 @@
 addition and 8-bit output, rotary positions, and linear attention with a decay a head.
 
 As in ``scan.py``, torch serves for device memory and streams only: the helpers check the
-tensors, allocate outputs (``out`` / the named buffers take the caller's), build the
-descriptor from sizes and strides and make one call of the C ABI (``include/ssm_scan.h``
-says what each computes).  Tensors may have any strides with a dense last dimension.  Calls
-go to ``stream`` (default: the current stream of the tensors' device, made current for the
-call where it is not).  Workspaces come from torch's allocator on that stream unless
-given; calls that overlap on the GPU, captured graphs among them, must not share one.
+tensors, allocate outputs (``out`` / the named buffers take the caller's) and make one call
+of the C ABI (``include/ssm_scan.h`` says what each computes).  Tensors may have any strides
+with a dense last dimension.  Calls go to ``stream`` (default: the current stream of the
+tensors' device, made current for the call where it is not).  Workspaces come from torch's
+allocator on that stream unless given; calls that overlap on the GPU, captured graphs among
+them, must not share one.
+
+What a call checks and derives from its tensors' shapes, strides and types (never from their
+contents or addresses) is kept for the next call with the same ones: the checks alone would
+take longer than the smallest kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 
 import torch
@@ -24,37 +29,69 @@ _SCALING = {"plain": abi.ROPE_PLAIN, "linear": abi.ROPE_LINEAR, "ntk": abi.ROPE_
             "bands": abi.ROPE_BANDS}
 QUANT_BLOCK_COLUMNS = 128
 
+_PLANS = {}
+_MOST_PLANS = 1024
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-class _Call:
-    """The device and stream of a call: ``tensors`` all live on ``first``'s device, which is
-    current inside, as is ``stream`` where one is given (torch's allocations inside are its)."""
 
-    def __init__(self, stream, first, *tensors):
-        if not first.is_cuda:
-            raise ValueError("every tensor must live on a CUDA device (no CPU path)")
-        dev = first.get_device()
-        for t in tensors:
-            if t is not None and (not t.is_cuda or t.get_device() != dev):
-                raise ValueError("the tensors of a call must share one CUDA device")
-        self.guards = []
-        if torch.cuda.current_device() != dev:
-            self.guards.append(torch.cuda.device(dev))
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=dev)
-            if stream.device_index != dev:
-                raise ValueError("the stream belongs to another device than the tensors")
-            self.guards.append(torch.cuda.stream(stream))
+class _Plan:
+    """Descriptor, device and sizes of a call, from its tensors' layouts."""
 
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+    __slots__ = ("dev", "desc", "lib", "ws", "size", "blocks", "outs")
 
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
-        return False
+
+def _sig(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _plan(key, make, *args):
+    p = _PLANS.get(key)
+    if p is None:
+        p = make(*args)
+        p.lib = abi.load_library()
+        if len(_PLANS) >= _MOST_PLANS:
+            _PLANS.clear()
+        _PLANS[key] = p
+    return p
+
+
+def _device(first, *tensors):
+    if not first.is_cuda:
+        raise ValueError("every tensor must live on a CUDA device (no CPU path)")
+    dev = first.get_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise ValueError("the tensors of a call must share one CUDA device")
+    return dev
+
+
+@contextlib.contextmanager
+def _elsewhere(dev, stream):
+    """Makes ``dev`` and ``stream`` current (torch's allocations inside are the stream's)."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield _raw_stream(dev)
+            return
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        if stream.device_index != dev:
+            raise ValueError("the stream belongs to another device than the tensors")
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+
+
+def _on_device(go, p, stream, *args):
+    """go(plan, raw stream, ...) on the plan's device and the caller's stream."""
+    if stream is None and _current_device() == p.dev:
+        return go(p, _raw_stream(p.dev), *args)
+    with _elsewhere(p.dev, stream) as st:
+        return go(p, st, *args)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _want(t, name, shape, dtype, dense=False):
@@ -74,17 +111,29 @@ def _io(t, name):
     return _DTYPES[t.dtype]
 
 
-def _workspace(nbytes, given, device):
+def _workspace(p, given):
+    """(address, bytes, what keeps it alive)"""
     if given is not None:
-        return given, given.numel() * given.element_size()
-    if nbytes == 0:
-        return None, 0
-    return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+        if given.get_device() != p.dev:
+            raise ValueError("the workspace must live on the tensors' device")
+        return given.data_ptr(), given.numel() * given.element_size(), given
+    if p.ws == 0:
+        return None, 0, None
+    w = torch.empty(p.ws, dtype=torch.uint8, device=p.dev)
+    return w.data_ptr(), p.ws, w
+
+
+def _dense_strides(shape):
+    s, out = 1, []
+    for n in reversed(shape):
+        out.append(s)
+        s *= max(n, 1)
+    return tuple(reversed(out))
 
 
 # ---- RMS norm --------------------------------------------------------------------------
 
-@dataclasses.dataclass
+@dataclasses.dataclass(slots=True)
 class Normed:
     """``r`` the residual stream (``x`` itself without a residual), ``y`` the norm in the I/O
     type, ``y8`` its e4m3 codes with fp32 ``scales`` ([..., 1] or [..., dim / 128]), ``rstd``
@@ -112,13 +161,54 @@ def _rows(t, name, dim):
     return dim if step is None else step
 
 
-def _norm_desc(like, dim, eps, quant, **strides):
-    d = abi.RmsnormDesc()
+def _norm_plan(like, eps, quant, weight, dev, **tensors):
+    """``like``: the tensor whose shape and type all others have; outputs not named are dense."""
+    dim = like.shape[-1]
+    if weight is not None:
+        _want(weight, "weight", (dim,), torch.float32, True)
+    p = _Plan()
+    p.dev, p.desc, p.ws = dev, abi.RmsnormDesc(), 0
+    d = p.desc
     d.rows, d.dim = like.numel() // dim if dim else 0, dim
     d.eps, d.dtype_io, d.quant = eps, _io(like, "x"), quant
-    for k, t in strides.items():
-        setattr(d, "stride_" + k, dim if t is None else _rows(t, k, dim))
-    return d
+    for f, _ in abi.RmsnormDesc._fields_:
+        if f.startswith("stride_"):
+            t = tensors.get(f[7:])
+            if t is not None:
+                _want(t, f[7:], like.shape, like.dtype)
+            setattr(d, f, dim if t is None else _rows(t, f[7:], dim))
+    return p
+
+
+def _norm_fwd_plan(x, weight, residual, r, eps, quant, want_y):
+    if quant not in _QUANT:
+        raise ValueError(f"quant must be None, 'row' or 'block', not {quant!r}")
+    if quant is None and want_y is False:
+        raise ValueError("without quant the norm itself is the output: want_y cannot be False")
+    dev = _device(x, weight, residual, r)
+    p = _norm_plan(x, eps, _QUANT[quant], weight, dev, x=x, residual=residual, r=r)
+    p.blocks = 0 if quant is None else x.shape[-1] // QUANT_BLOCK_COLUMNS if quant == "block" else 1
+    p.outs = quant is None if want_y is None else want_y
+    return p
+
+
+def _norm_fwd(p, st, x, weight, residual, r, want_rstd):
+    shape = x.shape
+    if r is None and residual is not None:
+        r = torch.empty(shape, dtype=x.dtype, device=p.dev)
+    out = Normed(x if r is None else r)
+    if p.outs:
+        out.y = torch.empty(shape, dtype=x.dtype, device=p.dev)
+    if p.blocks:
+        out.y8 = torch.empty(shape, dtype=torch.float8_e4m3fn, device=p.dev)
+        out.scales = torch.empty((*shape[:-1], p.blocks), dtype=torch.float32, device=p.dev)
+    if want_rstd:
+        out.rstd = torch.empty(shape[:-1], dtype=torch.float32, device=p.dev)
+    rc = p.lib.ssm_rmsnorm_fwd(p.desc, x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(r), _ptr(out.y),
+                               _ptr(out.y8), _ptr(out.scales), _ptr(out.rstd), st)
+    if rc:
+        abi._check(rc, "ssm_rmsnorm_fwd")
+    return out
 
 
 def rmsnorm(x, weight=None, residual=None, eps=1e-5, quant=None, want_y=None, want_rstd=False,
@@ -129,34 +219,31 @@ def rmsnorm(x, weight=None, residual=None, eps=1e-5, quant=None, want_y=None, wa
     ``quant``: None, "row" or "block" (128 columns) for e4m3 codes with scales; ``want_y``: also
     the unquantised norm (default: only without ``quant``); ``want_rstd`` for a later
     :func:`rmsnorm_backward`; ``r``: where the sum goes (may be ``x`` or ``residual``)."""
-    if quant not in _QUANT:
-        raise ValueError(f"quant must be None, 'row' or 'block', not {quant!r}")
-    dim, dt, shape = x.shape[-1], x.dtype, x.shape
-    _want(x, "x", shape, dt)
-    if weight is not None:
-        _want(weight, "weight", (dim,), torch.float32, True)
-    if residual is not None:
-        _want(residual, "residual", shape, dt)
-    if r is not None:
-        _want(r, "r", shape, dt)
-    want_y = quant is None if want_y is None else want_y
-    if quant is None and not want_y:
-        raise ValueError("without quant the norm itself is the output: want_y cannot be False")
-    with _Call(stream, x, weight, residual, r) as st:
-        if r is None and residual is not None:
-            r = torch.empty(shape, dtype=dt, device=x.device)
-        out = Normed(r=x if r is None else r)
-        if want_y:
-            out.y = torch.empty(shape, dtype=dt, device=x.device)
-        if quant is not None:
-            out.y8 = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
-            blocks = dim // QUANT_BLOCK_COLUMNS if quant == "block" else 1
-            out.scales = torch.empty(*shape[:-1], blocks, dtype=torch.float32, device=x.device)
-        if want_rstd:
-            out.rstd = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
-        d = _norm_desc(x, dim, eps, _QUANT[quant], x=x, residual=residual, r=r, y=out.y, y8=out.y8)
-        abi.ssm_rmsnorm_fwd(d, x, residual, weight, r, out.y, out.y8, out.scales, out.rstd, st)
-    return out
+    p = _plan(("norm", _sig(x), _sig(weight), _sig(residual), _sig(r), eps, quant, want_y),
+              _norm_fwd_plan, x, weight, residual, r, eps, quant, want_y)
+    return _on_device(_norm_fwd, p, stream, x, weight, residual, r, want_rstd)
+
+
+def _norm_bwd_plan(dy, r, weight, rstd, dr, dx):
+    dev = _device(r, dy, weight, rstd, dr, dx)
+    _want(rstd, "rstd", r.shape[:-1], torch.float32, True)
+    p = _norm_plan(r, 0.0, abi.QUANT_NONE, weight, dev, dy=dy, r=r, dr=dr, dx=dx)
+    p.ws = abi.ssm_rmsnorm_workspace_size(p.desc)
+    return p
+
+
+def _norm_bwd(p, st, dy, r, weight, rstd, dr, dx, want_dweight, workspace):
+    if dx is None:
+        dx = torch.empty(r.shape, dtype=r.dtype, device=p.dev)
+    dw, ws, n, keep = None, None, 0, None
+    if want_dweight:
+        dw = torch.empty(r.shape[-1], dtype=torch.float32, device=p.dev)
+        ws, n, keep = _workspace(p, workspace)
+    rc = p.lib.ssm_rmsnorm_bwd(p.desc, dy.data_ptr(), r.data_ptr(), _ptr(weight), rstd.data_ptr(),
+                               _ptr(dr), dx.data_ptr(), _ptr(dw), ws, n, st)
+    if rc:
+        abi._check(rc, "ssm_rmsnorm_bwd")
+    return dx, dw
 
 
 def rmsnorm_backward(dy, r, weight, rstd, dr=None, dx=None, want_dweight=None, workspace=None,
@@ -164,27 +251,10 @@ def rmsnorm_backward(dy, r, weight, rstd, dr=None, dx=None, want_dweight=None, w
     """(dx, dweight) for ``dy``, the gradient of the norm, and ``dr``, that of the residual
     stream behind it; ``r`` and ``rstd`` as :func:`rmsnorm` returned them.  dx is the gradient
     of ``x`` and of ``residual``; dweight (fp32) is None without a weight."""
-    dim, dt, shape = r.shape[-1], r.dtype, r.shape
-    _want(r, "r", shape, dt)
-    _want(dy, "dy", shape, dt)
-    _want(rstd, "rstd", shape[:-1], torch.float32, True)
-    if weight is not None:
-        _want(weight, "weight", (dim,), torch.float32, True)
-    if dr is not None:
-        _want(dr, "dr", shape, dt)
-    if dx is not None:
-        _want(dx, "dx", shape, dt)
-    want_dweight = weight is not None if want_dweight is None else want_dweight
-    with _Call(stream, r, dy, weight, rstd, dr, dx, workspace) as st:
-        if dx is None:
-            dx = torch.empty(shape, dtype=dt, device=r.device)
-        dw = torch.empty(dim, dtype=torch.float32, device=r.device) if want_dweight else None
-        d = _norm_desc(r, dim, 0.0, abi.QUANT_NONE, dy=dy, r=r, dr=dr, dx=dx)
-        ws, n = None, 0
-        if want_dweight:
-            ws, n = _workspace(abi.ssm_rmsnorm_workspace_size(d), workspace, r.device)
-        abi.ssm_rmsnorm_bwd(d, dy, r, weight, rstd, dr, dx, dw, ws, n, st)
-    return dx, dw
+    p = _plan(("norm'", _sig(dy), _sig(r), _sig(weight), _sig(rstd), _sig(dr), _sig(dx)),
+              _norm_bwd_plan, dy, r, weight, rstd, dr, dx)
+    return _on_device(_norm_bwd, p, stream, dy, r, weight, rstd, dr, dx,
+                      weight is not None if want_dweight is None else want_dweight, workspace)
 
 
 # ---- rotary positions ------------------------------------------------------------------
@@ -203,7 +273,7 @@ def rope_frequencies(rot_dim, base=10000.0, scaling="plain", factor=1.0, low_tur
     return torch.tensor(f, dtype=torch.float64, device=device)
 
 
-def _rope(call, q, k, freq, positions, layout, magnitude, q_out, k_out, stream):
+def _rope_plan(q, k, freq, positions, layout, magnitude, q_out, k_out):
     if layout not in _LAYOUT:
         raise ValueError(f"layout must be 'half' or 'pairs', not {layout!r}")
     first = q if q is not None else k
@@ -212,7 +282,9 @@ def _rope(call, q, k, freq, positions, layout, magnitude, q_out, k_out, stream):
     if first.dim() != 4:
         raise ValueError(f"q and k are [batch, seqlen, heads, headdim], not {tuple(first.shape)}")
     b, L, _, dim = first.shape
-    d = abi.RopeDesc()
+    p = _Plan()
+    p.dev, p.desc, p.ws = _device(first, q, k, freq, positions, q_out, k_out), abi.RopeDesc(), 0
+    d = p.desc
     d.batch, d.seqlen, d.headdim, d.rot_dim = b, L, dim, 2 * freq.numel()
     d.magnitude, d.layout, d.dtype_io = magnitude, _LAYOUT[layout], _io(first, "q")
     _want(freq, "freq", (freq.numel(),), torch.float64, True)
@@ -223,24 +295,30 @@ def _rope(call, q, k, freq, positions, layout, magnitude, q_out, k_out, stream):
             d.stride_pos[:] = 0, positions.stride(0)
         else:
             d.stride_pos[:] = positions.stride()
-    outs = []
-    with _Call(stream, first, q, k, freq, positions, q_out, k_out) as st:
-        for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-            if x is None:
-                if y is not None:
-                    raise ValueError(f"an output without its input: {name}")
-                outs.append(None)
-                continue
-            _want(x, name, (b, L, x.shape[2] if x.dim() == 4 else -1, dim), first.dtype)
-            if y is None:
-                y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            if y is not None:
+                raise ValueError(f"an output without its input: {name}")
+            continue
+        _want(x, name, (b, L, x.shape[2] if x.dim() == 4 else -1, dim), first.dtype)
+        if y is not None:
             _want(y, name + "_out", x.shape, x.dtype)
-            setattr(d, "nheads_" + name, x.shape[2])
-            getattr(d, "stride_" + name)[:] = x.stride()[:3]
-            getattr(d, f"stride_{name}_out")[:] = y.stride()[:3]
-            outs.append(y)
-        call(d, q, k, freq, positions, outs[0], outs[1], st)
-    return tuple(outs)
+        setattr(d, "nheads_" + name, x.shape[2])
+        getattr(d, "stride_" + name)[:] = x.stride()[:3]
+        getattr(d, f"stride_{name}_out")[:] = (_dense_strides(x.shape) if y is None else y.stride())[:3]
+    return p
+
+
+def _rope(p, st, inverse, q, k, freq, positions, q_out, k_out):
+    if q_out is None and q is not None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=p.dev)
+    if k_out is None and k is not None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=p.dev)
+    call = p.lib.ssm_rope_bwd if inverse else p.lib.ssm_rope_fwd
+    rc = call(p.desc, _ptr(q), _ptr(k), freq.data_ptr(), _ptr(positions), _ptr(q_out), _ptr(k_out), st)
+    if rc:
+        abi._check(rc, "ssm_rope_bwd" if inverse else "ssm_rope_fwd")
+    return q_out, k_out
 
 
 def rope(q, k, freq, positions=None, layout="half", magnitude=1.0, q_out=None, k_out=None,
@@ -250,37 +328,68 @@ def rope(q, k, freq, positions=None, layout="half", magnitude=1.0, q_out=None, k
     q, k: [batch, seqlen, heads, headdim] (either may be None); ``freq`` from
     :func:`rope_frequencies`; ``positions``: int64 [batch, seqlen] or [seqlen] (default 0, 1, ...);
     ``layout``: "half" pairs value i with i + rot / 2, "pairs" neighbours; outputs may be the inputs."""
-    return _rope(abi.ssm_rope_fwd, q, k, freq, positions, layout, magnitude, q_out, k_out, stream)
+    p = _plan(("rope", _sig(q), _sig(k), _sig(freq), _sig(positions), layout, magnitude, _sig(q_out), _sig(k_out)),
+              _rope_plan, q, k, freq, positions, layout, magnitude, q_out, k_out)
+    return _on_device(_rope, p, stream, False, q, k, freq, positions, q_out, k_out)
 
 
 def rope_backward(dq, dk, freq, positions=None, layout="half", magnitude=1.0, dq_out=None,
                   dk_out=None, stream=None):
     """Gradients of :func:`rope`'s inputs for those of its outputs."""
-    return _rope(abi.ssm_rope_bwd, dq, dk, freq, positions, layout, magnitude, dq_out, dk_out,
-                 stream)
+    p = _plan(("rope", _sig(dq), _sig(dk), _sig(freq), _sig(positions), layout, magnitude, _sig(dq_out), _sig(dk_out)),
+              _rope_plan, dq, dk, freq, positions, layout, magnitude, dq_out, dk_out)
+    return _on_device(_rope, p, stream, True, dq, dk, freq, positions, dq_out, dk_out)
 
 
 # ---- linear attention ------------------------------------------------------------------
 
-def _la_desc(q, k, v, log_decay, lengths, scale, route, **more):
+def _la_plan(which, q, k, v, log_decay, lengths, scale, route, states, more):
+    """``states``: (name, tensor or None); ``more``: (stride field, tensor or None for a dense
+    one, shape)."""
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k and v are [batch, seqlen, heads, headdim]")
     b, L, h, dk = q.shape
     g, dv = k.shape[2], v.shape[3]
+    p = _Plan()
+    p.dev = _device(q, k, v, log_decay, lengths, *(t for _, t in states), *(t for _, t, _ in more))
+    p.size = (b, h, dk, dv)
     _want(q, "q", q.shape, q.dtype)
     _want(k, "k", (b, L, g, dk), q.dtype)
     _want(v, "v", (b, L, g, dv), q.dtype)
     _want(log_decay, "log_decay", (h,), torch.float32, True)
     if lengths is not None:
         _want(lengths, "lengths", (b,), torch.int32, True)
-    d = abi.LinattnDesc()
+    for name, t in states:
+        if t is not None:
+            _want(t, name, p.size, torch.float32, True)
+    d = p.desc = abi.LinattnDesc()
     d.batch, d.seqlen, d.nheads, d.nheads_kv, d.dim_k, d.dim_v = b, L, h, g, dk, dv
     d.scale, d.dtype_io, d.route = dk ** -0.5 if scale is None else scale, _io(q, "q"), route
     d.stride_q[:], d.stride_k[:], d.stride_v[:] = q.stride()[:3], k.stride()[:3], v.stride()[:3]
-    for name, (t, shape) in more.items():
-        _want(t, name, shape, q.dtype)
-        getattr(d, "stride_" + name)[:] = t.stride()[:3]
-    return d
+    for name, t, shape in more:
+        if t is not None:
+            _want(t, name, shape, q.dtype)
+        getattr(d, "stride_" + name)[:] = (_dense_strides(shape) if t is None else t.stride())[:3]
+    p.ws = 0 if which is None else abi.ssm_linattn_workspace_size(d, which)
+    return p
+
+
+def _la_fwd_plan(q, k, v, log_decay, scale, state, lengths, out, state_out, route):
+    return _la_plan(abi.PASS_FWD, q, k, v, log_decay, lengths, scale, route,
+                    (("state", state), ("state_out", state_out)), (("o", out, (*q.shape[:3], v.shape[-1])),))
+
+
+def _la_fwd(p, st, q, k, v, log_decay, state, lengths, out, want_state, state_out, workspace):
+    if out is None:
+        out = torch.empty((*q.shape[:3], p.size[3]), dtype=q.dtype, device=p.dev)
+    if state_out is None and want_state:
+        state_out = torch.empty(p.size, dtype=torch.float32, device=p.dev)
+    ws, n, keep = _workspace(p, workspace)
+    rc = p.lib.ssm_linattn_fwd(p.desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                               _ptr(state), _ptr(lengths), out.data_ptr(), _ptr(state_out), ws, n, st)
+    if rc:
+        abi._check(rc, "ssm_linattn_fwd")
+    return out, state_out
 
 
 def linattn(q, k, v, log_decay, scale=None, state=None, lengths=None, out=None, want_state=True,
@@ -291,20 +400,33 @@ def linattn(q, k, v, log_decay, scale=None, state=None, lengths=None, out=None, 
     ``scale`` defaults to dim_k ** -0.5; ``state`` fp32 [B, H, dim_k, dim_v] enters (default
     zero); ``lengths`` int32 [B]: rows behind them are neither read nor written (``out``
     keeps them).  ``state_out`` takes the final state (may be ``state``)."""
-    b, L, h = q.shape[:3]
-    shape = (b, h, q.shape[3], v.shape[3])
-    for name, s in (("state", state), ("state_out", state_out)):
-        if s is not None:
-            _want(s, name, shape, torch.float32, True)
-    with _Call(stream, q, k, v, log_decay, state, lengths, out, state_out, workspace) as st:
-        if out is None:
-            out = torch.empty(b, L, h, v.shape[3], dtype=q.dtype, device=q.device)
-        if state_out is None and want_state:
-            state_out = torch.empty(shape, dtype=torch.float32, device=q.device)
-        d = _la_desc(q, k, v, log_decay, lengths, scale, route, o=(out, (b, L, h, v.shape[3])))
-        ws, n = _workspace(abi.ssm_linattn_workspace_size(d, abi.PASS_FWD), workspace, q.device)
-        abi.ssm_linattn_fwd(d, q, k, v, log_decay, state, lengths, out, state_out, ws, n, st)
-    return out, state_out
+    p = _plan(("la", _sig(q), _sig(k), _sig(v), _sig(log_decay), scale, _sig(state), _sig(lengths), _sig(out),
+               _sig(state_out), route),
+              _la_fwd_plan, q, k, v, log_decay, scale, state, lengths, out, state_out, route)
+    return _on_device(_la_fwd, p, stream, q, k, v, log_decay, state, lengths, out, want_state, state_out, workspace)
+
+
+def _la_bwd_plan(q, k, v, log_decay, do, scale, state, dstate, lengths, dq, dk, dv, route):
+    return _la_plan(abi.PASS_BWD, q, k, v, log_decay, lengths, scale, route, (("state", state), ("dstate", dstate)),
+                    (("o", do, (*q.shape[:3], v.shape[-1])), ("dq", dq, q.shape), ("dk", dk, k.shape),
+                     ("dv", dv, v.shape)))
+
+
+def _la_bwd(p, st, q, k, v, log_decay, do, state, dstate, lengths, dq, dk, dv, workspace):
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=p.dev)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=q.dtype, device=p.dev)
+    if dv is None:
+        dv = torch.empty(v.shape, dtype=q.dtype, device=p.dev)
+    din = torch.empty(p.size, dtype=torch.float32, device=p.dev)
+    ws, n, keep = _workspace(p, workspace)
+    rc = p.lib.ssm_linattn_bwd(p.desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                               _ptr(state), _ptr(lengths), do.data_ptr(), _ptr(dstate), dq.data_ptr(),
+                               dk.data_ptr(), dv.data_ptr(), din.data_ptr(), ws, n, st)
+    if rc:
+        abi._check(rc, "ssm_linattn_bwd")
+    return dq, dk, dv, din
 
 
 def linattn_backward(q, k, v, log_decay, do, scale=None, state=None, dstate=None, lengths=None,
@@ -312,32 +434,30 @@ def linattn_backward(q, k, v, log_decay, do, scale=None, state=None, dstate=None
     """(dq, dk, dv, dstate): gradients of :func:`linattn` for ``do`` and ``dstate``, that of the
     final state (default zero); the returned dstate is that of the entering ``state``.
     ``out``: buffers (dq, dk, dv), whose rows behind ``lengths`` stay as they are."""
-    b, L, h = q.shape[:3]
-    shape = (b, h, q.shape[3], v.shape[3])
-    for name, s in (("state", state), ("dstate", dstate)):
-        if s is not None:
-            _want(s, name, shape, torch.float32, True)
     dq, dk, dv = out if out is not None else (None, None, None)
-    with _Call(stream, q, k, v, log_decay, do, state, dstate, lengths, dq, dk, dv, workspace) as st:
-        dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
-                      for x, y in ((q, dq), (k, dk), (v, dv)))
-        din = torch.empty(shape, dtype=torch.float32, device=q.device)
-        d = _la_desc(q, k, v, log_decay, lengths, scale, route, o=(do, (b, L, h, v.shape[3])),
-                     dq=(dq, q.shape), dk=(dk, k.shape), dv=(dv, v.shape))
-        ws, n = _workspace(abi.ssm_linattn_workspace_size(d, abi.PASS_BWD), workspace, q.device)
-        abi.ssm_linattn_bwd(d, q, k, v, log_decay, state, lengths, do, dstate, dq, dk, dv, din, ws,
-                            n, st)
-    return dq, dk, dv, din
+    p = _plan(("la'", _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(do), scale, _sig(state), _sig(dstate),
+               _sig(lengths), _sig(dq), _sig(dk), _sig(dv), route),
+              _la_bwd_plan, q, k, v, log_decay, do, scale, state, dstate, lengths, dq, dk, dv, route)
+    return _on_device(_la_bwd, p, stream, q, k, v, log_decay, do, state, dstate, lengths, dq, dk, dv, workspace)
+
+
+def _la_step_plan(q, k, v, log_decay, state, scale, out):
+    return _la_plan(None, q, k, v, log_decay, None, scale, abi.LINATTN_AUTO, (("state", state),),
+                    (("o", out, (*q.shape[:3], v.shape[-1])),))
+
+
+def _la_step(p, st, q, k, v, log_decay, state, out):
+    if out is None:
+        out = torch.empty((*q.shape[:3], p.size[3]), dtype=q.dtype, device=p.dev)
+    rc = p.lib.ssm_linattn_step(p.desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                state.data_ptr(), out.data_ptr(), st)
+    if rc:
+        abi._check(rc, "ssm_linattn_step")
+    return out
 
 
 def linattn_step(q, k, v, log_decay, state, scale=None, out=None, stream=None):
     """o [B, 1, H, dim_v] of one token (seqlen 1); ``state`` is updated in place."""
-    b, L, h = q.shape[:3]
-    _want(state, "state", (b, h, q.shape[3], v.shape[3]), torch.float32, True)
-    with _Call(stream, q, k, v, log_decay, state, out) as st:
-        if out is None:
-            out = torch.empty(b, L, h, v.shape[3], dtype=q.dtype, device=q.device)
-        d = _la_desc(q, k, v, log_decay, None, scale, abi.LINATTN_AUTO,
-                     o=(out, (b, L, h, v.shape[3])))
-        abi.ssm_linattn_step(d, q, k, v, log_decay, state, out, st)
-    return out
+    p = _plan(("la1", _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(state), scale, _sig(out)),
+              _la_step_plan, q, k, v, log_decay, state, scale, out)
+    return _on_device(_la_step, p, stream, q, k, v, log_decay, state, out)
