@@ -16,12 +16,16 @@
 // A block walks one segment of one (batch row, head), 64 columns of v and the state: per
 // chunk 80 KB come in by TMA and 16 KB go out.  One block an SM, its 20 warps with a role each:
 //     warp 0       TMA loads, two chunks ahead, each tile again as soon as its last reader is done
-//     warp 1       all MMAs, per chunk: A K^T, K^T V', A S, P V
+//     warp 1       all MMAs, per chunk: K^T V', A S, the next chunk's A K^T, P V
+//     warp 2       TMA stores of the output, which is laid over the chunk's V tile
 //     warps 4-11   P from the scores, and the output (a thread a token and half of the columns)
 //     warps 12-15  the state (a thread a state row, 64 values in registers)
-//     warps 16-19  V'
+//     warps 16-19  V', in halves of 64 tokens
 // so that P is made while K^T V' and A S run, and V', the state and the output of one chunk
-// beside the products of the next.
+// beside the products of the next.  Every role runs its own code once a chunk, so the walk is
+// compiled for each direction and kind of output and its loops stay rolled: instruction fetch
+// was what bound a kernel of the same structure with unrolled, run-time variants (185 KB of
+// code, 613 us for 4 x 16384 tokens of 16 heads; 72 KB, 412 us).
 #include <atomic>
 
 #include "chunk_common.cuh"
@@ -62,11 +66,10 @@ constexpr uint32_t TM_P = 448;           // 64: P, two bf16 a column
 constexpr uint32_t TM_COLS = 512;
 
 struct Maps {
-    CUtensorMap a, k, v;
+    CUtensorMap a, k, v, o;
 };
 struct Args {
     LaArgs p;
-    int o32[3];      // the output takes 32-byte stores
     float *seg[3];   // [segment][b H + h][da][dc]: what a segment adds, then its entering state
     int nseg, G;     // segments of G chunks
     int slices;      // 64-column slices, the most of all walks
@@ -78,6 +81,15 @@ template <uint32_t LBO> __device__ __forceinline__ uint64_t desc(uint32_t units)
     constexpr uint32_t hi = (1024u >> 4) | 1u << 14 | LAYOUT_SW128 << 29;
     return (uint64_t)hi << 32 | (units | (LBO >> 4) << 16);
 }
+// Prefetch of a tile into L2.
+__device__ __forceinline__ void tma_prefetch_4d(const void *tmap, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];\n" ::"l"(
+                     reinterpret_cast<uint64_t>(tmap)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+}
+// every committed bulk store has reached memory
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
 // One lane of a converged warp, known to the compiler to be one.
 __device__ __forceinline__ bool elect_one() {
     uint32_t one;
@@ -98,35 +110,50 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
-#define LA_R16(r) \
-    "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), \
-    "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-// 32 columns of the thread's lane; the values are there after tmem_wait_ld
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&a)[16], uint32_t (&b)[16]) {
+// Loads from tensor memory write their registers at any time up to the wait, behind the
+// compiler's back: a copy or a reuse of one of them in between reads or destroys a value.
+// So each load and its wait are one statement.  Columns of the thread's lane:
+#define LA_OUT8(r, k) \
+    "=&r"(r[k]), "=&r"(r[k + 1]), "=&r"(r[k + 2]), "=&r"(r[k + 3]), "=&r"(r[k + 4]), "=&r"(r[k + 5]), "=&r"(r[k + 6]), "=&r"(r[k + 7])
+// 32 columns
+__device__ __forceinline__ void tmem_get32(uint32_t t, uint32_t (&a)[16], uint32_t (&b)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        : LA_R16(a), LA_R16(b)
-        : "r"(taddr));
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : LA_OUT8(a, 0), LA_OUT8(a, 8), LA_OUT8(b, 0), LA_OUT8(b, 8)
+        : "r"(t)
+        : "memory");
 }
-// (the values pass through, so that nothing reads them before)
-#define LA_IO16(r) \
-    "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), \
-    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&a)[16], uint32_t (&b)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;\n" : LA_IO16(a), LA_IO16(b)::"memory");
+// 16 columns at each of two places
+__device__ __forceinline__ void tmem_get16x2(uint32_t t, uint32_t u, uint32_t (&a)[16], uint32_t (&b)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+        "%29,%30,%31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : LA_OUT8(a, 0), LA_OUT8(a, 8), LA_OUT8(b, 0), LA_OUT8(b, 8)
+        : "r"(t), "r"(u)
+        : "memory");
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
+// 8 columns at each of two places
+__device__ __forceinline__ void tmem_get8x2(uint32_t t, uint32_t u, uint32_t (&a)[8], uint32_t (&b)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : LA_OUT8(a, 0), LA_OUT8(b, 0)
+        : "r"(t), "r"(u)
+        : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld8(uint32_t (&r)[8], uint32_t (&q)[8], uint32_t (&t)[8]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(q[0]), "+r"(q[1]), "+r"(q[2]), "+r"(q[3]), "+r"(q[4]), "+r"(q[5]), "+r"(q[6]), "+r"(q[7]),
-                   "+r"(t[0]), "+r"(t[1]), "+r"(t[2]), "+r"(t[3]), "+r"(t[4]), "+r"(t[5]), "+r"(t[6]), "+r"(t[7])
-                 :: "memory");
+__device__ __forceinline__ void tmem_get8(uint32_t t, uint32_t (&a)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : LA_OUT8(a, 0)
+        : "r"(t)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -150,25 +177,36 @@ __device__ __forceinline__ uint32_t high2(float a, float b) {
 }
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-// (a.x b.x, a.y b.y) in one instruction
+// two products, sums or both in one instruction
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t &>(r))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
-__device__ __forceinline__ void st32(void *p, uint4 a, uint4 b) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
-                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-                 : "memory");
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
 }
-
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 asf2(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
 struct Bars {
     uint64_t a_full[2], k_full[2], v_full[2];   // tiles loaded
     uint64_t a_free[2], k_free[2], v_free[2];   // tiles read by their last product
-    uint64_t sc, kv, o;                         // products done: scores; K^T V'; A S and P V
-    uint64_t p, vp, s;                          // operands written: P, V', S
-    uint64_t kv_read, o_read;                   // results fetched from tensor memory
+    uint64_t sc, kv[2], o;                      // products done: scores; K^T V' (halves of the tokens); A S and P V
+    uint64_t p, vp[2], s;                       // operands written: P, V' (halves), S
+    uint64_t sc_read, kv_read, o_read;          // results fetched from tensor memory
+    uint64_t o_tile;                            // the output in shared memory, or stored
     uint64_t end;
     uint32_t tslot;
     int abort;
@@ -180,23 +218,31 @@ static_assert(sizeof(Bars) <= 224, "barrier space");
 // hint lets the hardware keep the thread suspended: polls of 16 waiting warps would take the
 // issue slots that the others need.
 constexpr uint32_t POLL_NS = 20000, POLLS = 1u << 15;   // about half a second
-__device__ __forceinline__ bool await(Bars *B, uint64_t *bar, uint32_t n) {
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(POLL_NS)
+        : "memory");
+    return ok != 0;
+}
+// (`last`: a wait for what is in flight when the block ends, whatever the others do)
+__device__ __noinline__ bool poll_on(Bars *B, uint32_t bar, uint32_t parity, bool last) {
 #pragma unroll 1
     for (uint32_t i = 0; i < POLLS; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}\n"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(n & 1u), "r"(POLL_NS)
-            : "memory");
-        if (ok) return true;
-        if (*reinterpret_cast<volatile int *>(&B->abort)) return false;
+        if (poll(bar, parity)) return true;
+        if (!last && *reinterpret_cast<volatile int *>(&B->abort)) return false;
     }
     *reinterpret_cast<volatile int *>(&B->abort) = 1;
     atomicCAS(&ssm_la_error_word, 0, 1);
     return false;
+}
+__device__ __forceinline__ bool await(Bars *B, uint64_t *bar, uint32_t n) {
+    const uint32_t a = smem_u32(bar);
+    return poll(a, n & 1u) || poll_on(B, a, n & 1u, false);
 }
 // The same for a whole warp, all lanes alike.
 __device__ __forceinline__ bool await_warp(Bars *B, uint64_t *bar, uint32_t n) {
@@ -208,54 +254,28 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// STATE: only the state is walked (no scores, no output).
-template <bool STATE>
-__global__ void __launch_bounds__(THREADS, 1)
-k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
-          const __grid_constant__ Maps m2, const __grid_constant__ Args A) {
+// The walk of a block.  STATE: only the state (no scores, no output).  REV: reverse.  OUT: the
+// output is bf16 (0) or fp32 (1).
+template <bool STATE, bool REV, int OUT>
+__device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWalk &w, int wi, int slice, int bh, int sg,
+                                     unsigned char *sm) {
     const LaArgs &p = A.p;
-    const int BH = p.B * p.H;
-    int id = blockIdx.x;
-    const int slice = id % A.slices;
-    id /= A.slices;
-    const int bh = id % BH;
-    id /= BH;
-    const int sg = id % A.nseg, wi = id / A.nseg;
-    const LaWalk &w = p.w[wi];
-    const Maps *maps = wi == 0 ? &m0 : wi == 1 ? &m1 : &m2;
-    const int c0 = 64 * slice;
-    if (c0 >= w.dc) return;
+    const int c0 = 64 * slice, BH = p.B * p.H;
     const int b = bh / p.H, h = bh - b * p.H;
     const int len = p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L;
     const int first = sg * A.G, nch = min(A.G, (len + C - 1) / C - first);   // chunks; may be <= 0
-    const bool rev = w.rev;
-
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *sm = reinterpret_cast<unsigned char *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *f32 = reinterpret_cast<float *>(sm + SM_F32);
     Bars *B = reinterpret_cast<Bars *>(sm + SM_BAR);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i)
-            for (uint64_t *q : {&B->a_full[i], &B->k_full[i], &B->v_full[i], &B->a_free[i], &B->k_free[i], &B->v_free[i]})
-                mbar_init(q, 1);
-        for (uint64_t *q : {&B->sc, &B->kv, &B->o, &B->end}) mbar_init(q, 1);
-        for (uint64_t *q : {&B->vp, &B->s, &B->kv_read}) mbar_init(q, 4);    // an arrival a warp
-        for (uint64_t *q : {&B->p, &B->o_read}) mbar_init(q, 8);
-        B->abort = 0;
-        mbar_fence_init();
-    }
-    if (warp == 1) tmem_alloc(&B->tslot, TM_COLS);
     {   // powers of lam from its logarithm in 64 bits: every one right to half a step
         double g = (double)p.log_decay[h];
         if (g < -1e6) g = -1e6;   // -inf: lam^0 stays 1
         const double rw = (double)w.read * (double)w.write;
-        for (int i = tid; i < 129 + 160 + 64; i += THREADS) {
-            if (i < 129) f32[F_PW + i] = (float)exp(g * i);
-            else if (i < 289) f32[F_W + i - 129] = i < 161 ? 0.f : (float)(rw * exp(g * (i - 161)));
-            else if (i < 321) f32[F_UP + i - 289] = (float)exp(g * (i - 289));
-            else f32[F_DOWN + i - 321] = (float)exp(g * (352 - i));
+        if (tid < 129 + 160 + 64) {
+            const int m = tid < 129 ? tid : tid < 289 ? tid - 161 : tid < 321 ? tid - 289 : 352 - tid;
+            const double e = exp(g * m);
+            f32[tid < 129 ? F_PW + tid : tid < 289 ? F_W + tid - 129 : tid < 321 ? F_UP + tid - 289 : F_DOWN + tid - 321] =
+                m < 0 ? 0.f : (float)(tid >= 129 && tid < 289 ? rw * e : e);
         }
     }
     fence_before_sync();
@@ -265,10 +285,8 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
     const uint32_t lane_q = (uint32_t)(32 * (warp & 3)) << 16;
     const int row = 32 * (warp & 3) + lane;      // token, or state row, of the thread
     // chunk number c of the walk: its first token and its tokens
-    auto chunk = [&](int c) { return C * (first + (rev ? nch - 1 - c : c)); };
+    auto chunk = [&](int c) { return C * (first + (REV ? nch - 1 - c : c)); };
     auto ntok = [&](int t0) { return min(C, len - t0); };
-    // rows of the chunk's tiles that are other tokens (TMA fills those past L with zeros)
-    auto dirty = [&](int t0, int n) { return n < C && t0 + n < p.L; };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -279,29 +297,38 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
                 const int s = c & 1, t0 = chunk(c);
                 const uint32_t n = (uint32_t)(c >> 1) - 1u;
                 unsigned char *st = sm + s * STAGE;
+                if (c + 2 < nch) {   // what comes into these slots next, on its way into L2
+                    const int tn = chunk(c + 2);
+                    tma_prefetch_4d(&maps.k, 0, hk, tn, b);
+                    if (w.da > 64) tma_prefetch_4d(&maps.k, 64, hk, tn, b);
+                    if (!STATE)
+                        for (int i = 0; i < nboxa; ++i) tma_prefetch_4d(&maps.a, 64 * i, ha, tn, b);
+                    tma_prefetch_4d(&maps.v, c0, hv, tn, b);
+                }
                 if (c >= 2 && !await(B, &B->k_free[s], n)) break;
                 mbar_expect_tx(&B->k_full[s], 2 * TILE);
-                tma_load_4d(st + ST_K, &maps->k, &B->k_full[s], 0, hk, t0, b);
+                tma_load_4d(st + ST_K, &maps.k, &B->k_full[s], 0, hk, t0, b);
                 // a second box past the head is zeros: state rows that are not there
-                tma_load_4d(st + ST_K + TILE, &maps->k, &B->k_full[s], 64, hk, t0, b);
+                tma_load_4d(st + ST_K + TILE, &maps.k, &B->k_full[s], 64, hk, t0, b);
                 ++got_k;
                 if (!STATE) {
                     if (c >= 2 && !await(B, &B->a_free[s], n)) break;
                     mbar_expect_tx(&B->a_full[s], TILE * nboxa);
                     for (int i = 0; i < nboxa; ++i)
-                        tma_load_4d(st + ST_A + i * TILE, &maps->a, &B->a_full[s], 64 * i, ha, t0, b);
+                        tma_load_4d(st + ST_A + i * TILE, &maps.a, &B->a_full[s], 64 * i, ha, t0, b);
                     ++got_a;
                 }
                 if (c >= 2 && !await(B, &B->v_free[s], n)) break;
                 mbar_expect_tx(&B->v_full[s], TILE);
-                tma_load_4d(st + ST_V, &maps->v, &B->v_full[s], c0, hv, t0, b);
+                tma_load_4d(st + ST_V, &maps.v, &B->v_full[s], c0, hv, t0, b);
                 ++got_v;
             }
             // no copy is in flight when the block ends
-            for (uint32_t i = 0; i < 2; ++i) {
-                if (got_a > i) mbar_wait(&B->a_full[(got_a - 1 - i) & 1], ((got_a - 1 - i) >> 1) & 1u, WAIT_LIMIT);
-                if (got_k > i) mbar_wait(&B->k_full[(got_k - 1 - i) & 1], ((got_k - 1 - i) >> 1) & 1u, WAIT_LIMIT);
-                if (got_v > i) mbar_wait(&B->v_full[(got_v - 1 - i) & 1], ((got_v - 1 - i) >> 1) & 1u, WAIT_LIMIT);
+#pragma unroll 1
+            for (uint32_t i = 0; i < 6; ++i) {
+                const uint32_t got = i < 2 ? got_a : i < 4 ? got_k : got_v, back = 1 + (i & 1);
+                uint64_t *full = i < 2 ? B->a_full : i < 4 ? B->k_full : B->v_full;
+                if (got >= back) poll_on(B, smem_u32(&full[(got - back) & 1]), ((got - back) >> 1) & 1u, true);
             }
         }
         __syncwarp();
@@ -315,52 +342,82 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
             auto kmaj = [&](uint32_t tile, int s) { return desc<16u>(u0 + (tile >> 4) + (s >> 2) * (TILE >> 4) + (s & 3) * 2u); };
             auto mnmaj = [&](uint32_t tile, int s) { return desc<TILE>(u0 + (tile >> 4) + 128u * s); };
             const int ks = (w.da + 15) / 16;
-#pragma unroll 1
-            for (int c = 0; c < nch; ++c) {
+            auto scores = [&](int c) {
                 const uint32_t st = (c & 1) ? STAGE : 0u;
-                const uint32_t half = (uint32_t)c >> 1;
-                if (!await(B, &B->k_full[c & 1], half)) break;
-                if (!STATE) {
-                    if (!await(B, &B->a_full[c & 1], half)) break;
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        if (s < ks) mma_bf16(tm + TM_SC, kmaj(st + ST_A, s), kmaj(st + ST_K, s), id_sc, s > 0);
-                    mma_commit(&B->sc);
-                }
-                if (!await(B, &B->vp, (uint32_t)c)) break;
-                if (c > 0 && !await(B, &B->kv_read, (uint32_t)c - 1u)) break;
+                if (!await(B, &B->k_full[c & 1], (uint32_t)c >> 1) || !await(B, &B->a_full[c & 1], (uint32_t)c >> 1)) return false;
+                if (c > 0 && !await(B, &B->sc_read, (uint32_t)c - 1u)) return false;
                 fence_after_sync();
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    mma_bf16(tm + TM_KV, mnmaj(st + ST_K, s), mnmaj(SM_VP, s), id_kv, s > 0);
-                mma_commit(&B->kv);
-                mma_commit(&B->k_free[c & 1]);
-                if (!STATE) {
-                    if (!await(B, &B->s, (uint32_t)c)) break;
-                    if (c > 0 && !await(B, &B->o_read, (uint32_t)c - 1u)) break;
-                    fence_after_sync();
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        if (s < ks) mma_bf16(tm + TM_OS, kmaj(st + ST_A, s), mnmaj(SM_S, s), id_n, s > 0);
-                    mma_commit(&B->a_free[c & 1]);
-                    if (!await(B, &B->p, (uint32_t)c)) break;
-                    fence_after_sync();
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        mma_bf16_ts(tm + TM_OI, tm + TM_P + 8u * s, mnmaj(st + ST_V, s), id_n, s > 0);
-                    mma_commit(&B->o);
+#pragma unroll 1
+                for (int s = 0; s < ks; ++s)
+                    mma_bf16(tm + TM_SC, kmaj(st + ST_A, s), kmaj(st + ST_K, s), id_sc, s > 0);
+                mma_commit(&B->sc);
+                return true;
+            };
+            bool ok = true;
+#pragma unroll 1
+            for (int c = STATE ? 0 : -1; c < nch; ++c) {
+                const uint32_t st = (c & 1) ? STAGE : 0u;
+                if (c >= 0) {
+                    if (STATE && !await(B, &B->k_full[c & 1], (uint32_t)c >> 1)) break;
+                    if (c > 0 && !await(B, &B->kv_read, (uint32_t)c - 1u)) break;
+#pragma unroll 1
+                    for (int z = 0; z < 2; ++z) {
+                        if (!(ok = await(B, &B->vp[z], (uint32_t)c))) break;
+                        fence_after_sync();
+#pragma unroll 1
+                        for (int s = 0; s < 4; ++s)
+                            mma_bf16(tm + TM_KV, mnmaj(st + ST_K, 4 * z + s), mnmaj(SM_VP, 4 * z + s), id_kv, z > 0 || s > 0);
+                        mma_commit(&B->kv[z]);
+                    }
+                    if (!ok) break;
+                    mma_commit(&B->k_free[c & 1]);
+                    if (!STATE) {
+                        if (!await(B, &B->s, (uint32_t)c)) break;
+                        if (c > 0 && !await(B, &B->o_read, (uint32_t)c - 1u)) break;
+                        fence_after_sync();
+#pragma unroll 1
+                        for (int s = 0; s < ks; ++s)
+                            mma_bf16(tm + TM_OS, kmaj(st + ST_A, s), mnmaj(SM_S, s), id_n, s > 0);
+                        mma_commit(&B->a_free[c & 1]);
+                    }
                 }
-                mma_commit(&B->v_free[c & 1]);
+                if (!STATE) {
+                    if (c + 1 < nch && !scores(c + 1)) break;
+                    if (c >= 0) {
+                        if (!await(B, &B->p, (uint32_t)c)) break;
+                        fence_after_sync();
+#pragma unroll 1
+                        for (int s = 0; s < 8; ++s)
+                            mma_bf16_ts(tm + TM_OI, tm + TM_P + 8u * s, mnmaj(st + ST_V, s), id_n, s > 0);
+                        mma_commit(&B->o);
+                    }
+                }
+                if (STATE) mma_commit(&B->v_free[c & 1]);   // else warp 2, when the output has left it
             }
             mma_commit(&B->end);   // every MMA is over before tensor memory goes
-            mbar_wait(&B->end, 0u, WAIT_LIMIT);
+            poll_on(B, smem_u32(&B->end), 0u, true);
+        }
+        __syncwarp();
+    } else if (!STATE && warp == 2) {
+        if (lane == 0) {
+#pragma unroll 1
+            for (int c = 0; c < nch; ++c) {
+                const int t0 = chunk(c), n = ntok(t0);
+                if (!await(B, &B->o_tile, (uint32_t)c)) break;
+                if (OUT == 0 && !(n < C && t0 + n < p.L)) {   // what is past L or the head is not written
+                    tma_store_4d(&maps.o, sm + (c & 1) * STAGE + ST_V, c0, h, t0, b);
+                    bulk_commit();
+                    bulk_wait_read_all();
+                }
+                mbar_arrive(&B->v_free[c & 1]);
+            }
+            bulk_wait_all();
         }
         __syncwarp();
     } else if (!STATE && warp >= 4 && warp < 12) {
         const int half = (warp - 4) >> 2, qd = warp & 3;
         const long long ob = b * w.so[0] + h * w.so[2] + c0 + 32 * half;
         const int nq = min(4, (w.dc - c0 - 32 * half) / 8);   // 8-column pieces of the output (<= 0: none)
-        const bool wide = A.o32[wi] && nq == 4;
 #pragma unroll 1
         for (int c = 0; c < nch; ++c) {
             const int t0 = chunk(c), n = ntok(t0);
@@ -372,43 +429,46 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
             for (int z = 0; z < 2; ++z) {
                 const int jb = 2 * half + z;
                 uint32_t o[16];
-                if (rev ? jb < qd : jb > qd) {   // masked
+                const bool zero = REV ? jb < qd : jb > qd;   // masked
+                uint32_t x[16], y[16];
+                if (!zero) {
+                    tmem_get32(tm + TM_SC + lane_q + 32u * jb, x, y);
+                }
+                if (z == 1) {
+                    fence_before_sync();
+                    warp_arrive(&B->sc_read);
+                }
+                if (zero) {
 #pragma unroll
                     for (int u = 0; u < 16; ++u) o[u] = 0u;
-                } else {
-                    uint32_t x[16], y[16];
-                    tmem_ld32(tm + TM_SC + lane_q + 32u * jb, x, y);
-                    const int left = n - 32 * jb;   // columns of this sequence
-                    if (jb == qd || left < 32) {
-                        // the diagonal, and the sequence's end: tokens past it are not read, whatever they hold
-                        const int at = rev ? 32 * jb - row : row - 32 * jb, d = rev ? 1 : -1;
-                        float wv[32];
+                } else if (jb == qd) {   // the diagonal
+                    const int d = REV ? 1 : -1;
+                    const float *wv = f32 + F_W + 32 + (REV ? 32 * jb - row : row - 32 * jb);
 #pragma unroll
-                        for (int u = 0; u < 32; ++u) wv[u] = f32[F_W + 32 + at + d * u];
-                        tmem_wait_ld(x, y);
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            o[u] = pack2(2 * u < left ? __uint_as_float(x[2 * u]) * wv[2 * u] : 0.f,
-                                         2 * u + 1 < left ? __uint_as_float(x[2 * u + 1]) * wv[2 * u + 1] : 0.f);
-                            o[8 + u] = pack2(16 + 2 * u < left ? __uint_as_float(y[2 * u]) * wv[16 + 2 * u] : 0.f,
-                                             17 + 2 * u < left ? __uint_as_float(y[2 * u + 1]) * wv[17 + 2 * u] : 0.f);
-                        }
-                    } else {
-                        // off it the weight is a factor of the row times one of the column
-                        const float r = f32[F_W + 32 + (rev ? 32 * jb - row : row - 32 * jb - 31)];
-                        const float4 *cw = reinterpret_cast<const float4 *>(f32 + (rev ? F_UP : F_DOWN));
-                        const float2 rr = make_float2(r, r);
-                        tmem_wait_ld(x, y);
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const float4 f = cw[u];
-                            const uint32_t *s4 = u < 4 ? x + 4 * u : y + 4 * (u - 4);
-                            const float2 e0 = mul2(mul2(make_float2(__uint_as_float(s4[0]), __uint_as_float(s4[1])), rr), make_float2(f.x, f.y));
-                            const float2 e1 = mul2(mul2(make_float2(__uint_as_float(s4[2]), __uint_as_float(s4[3])), rr), make_float2(f.z, f.w));
-                            o[2 * u] = pack2(e0.x, e0.y);
-                            o[2 * u + 1] = pack2(e1.x, e1.y);
-                        }
+                    for (int u = 0; u < 16; ++u) {
+                        const float2 e = mul2(u < 8 ? asf2(x[2 * u], x[2 * u + 1]) : asf2(y[2 * u - 16], y[2 * u - 15]),
+                                              make_float2(wv[0], wv[d]));
+                        wv += 2 * d;
+                        o[u] = pack2(e.x, e.y);
                     }
+                } else {   // off it the weight is a factor of the row times one of the column
+                    const float r = f32[F_W + 32 + (REV ? 32 * jb - row : row - 32 * jb - 31)];
+                    const float4 *cw = reinterpret_cast<const float4 *>(f32 + (REV ? F_UP : F_DOWN));
+                    const float2 rr = make_float2(r, r);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const float4 f = cw[u];
+                        const uint32_t *s4 = u < 4 ? x + 4 * u : y + 4 * (u - 4);
+                        const float2 e0 = mul2(mul2(asf2(s4[0], s4[1]), rr), make_float2(f.x, f.y));
+                        const float2 e1 = mul2(mul2(asf2(s4[2], s4[3]), rr), make_float2(f.z, f.w));
+                        o[2 * u] = pack2(e0.x, e0.y);
+                        o[2 * u + 1] = pack2(e1.x, e1.y);
+                    }
+                }
+                const int left = n - 32 * jb;   // columns of this sequence
+                if (left < 32) {   // tokens past it do not count, whatever they hold
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) o[u] = 2 * u + 1 < left ? o[u] : 2 * u < left ? o[u] & 0xffffu : 0u;
                 }
                 tmem_st16(tm + TM_P + lane_q + 16u * jb, o);
             }
@@ -417,117 +477,62 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
             warp_arrive(&B->p);
             if (!await_warp(B, &B->o, (uint32_t)c)) break;
             fence_after_sync();
-            uint32_t x[16], y[16], u[16], v[16];
-            tmem_ld32(tm + TM_OI + lane_q + 32u * half, x, y);
-            tmem_ld32(tm + TM_OS + lane_q + 32u * half, u, v);
-            const float e = w.read * f32[F_PW + max(0, rev ? n - 1 - row : row + 1)];
-            tmem_wait_ld(x, y);
-            tmem_wait_ld(u, v);
-            fence_before_sync();
-            warp_arrive(&B->o_read);
-            float o[32];
+            const float e = w.read * f32[F_PW + max(0, REV ? n - 1 - row : row + 1)];
+            const float2 ee = make_float2(e, e);
+            // 16 columns at a time: over the chunk's V tile, from where warp 2 stores whole chunks, or,
+            // where rows behind the sequence must stay as they are, straight to memory
+            const bool tile = OUT == 0 && !(n < C && t0 + n < p.L);
+            unsigned char *vt = sm + (c & 1) * STAGE + ST_V + row * 128;
+            const long long at = ob + (long long)(t0 + row) * w.so[1];
+#pragma unroll 1
+            for (int z = 0; z < 2; ++z) {
+                uint32_t x[16], u[16];
+                tmem_get16x2(tm + TM_OI + lane_q + 32u * half + 16u * z, tm + TM_OS + lane_q + 32u * half + 16u * z, x, u);
+                float2 o[8];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                o[j] = fmaf(e, __uint_as_float(u[j]), __uint_as_float(x[j]));
-                o[16 + j] = fmaf(e, __uint_as_float(v[j]), __uint_as_float(y[j]));
-            }
-            if (row < n) {
-                const long long at = ob + (long long)(t0 + row) * w.so[1];
-                if (w.o_f32) {
-                    float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(w.o) + at);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (q < 2 * nq) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-                } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(w.o) + at);
-                    uint4 r[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        r[q] = make_uint4(pack2(o[8 * q], o[8 * q + 1]), pack2(o[8 * q + 2], o[8 * q + 3]),
-                                          pack2(o[8 * q + 4], o[8 * q + 5]), pack2(o[8 * q + 6], o[8 * q + 7]));
-                    if (wide) {
-                        st32(dst, r[0], r[1]);
-                        st32(dst + 2, r[2], r[3]);
-                    } else {
+                for (int j = 0; j < 8; ++j) o[j] = fma2(ee, asf2(u[2 * j], u[2 * j + 1]), asf2(x[2 * j], x[2 * j + 1]));
+                if (OUT == 1) {
+                    if (row < n) {
+                        float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(w.o) + at) + 4 * z;
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            if (q < nq) dst[q] = r[q];
+                            if (q < 2 * nq - 4 * z) dst[q] = make_float4(o[2 * q].x, o[2 * q].y, o[2 * q + 1].x, o[2 * q + 1].y);
                     }
+                    continue;
+                }
+                const uint4 r0 = make_uint4(pack2(o[0].x, o[0].y), pack2(o[1].x, o[1].y), pack2(o[2].x, o[2].y), pack2(o[3].x, o[3].y));
+                const uint4 r1 = make_uint4(pack2(o[4].x, o[4].y), pack2(o[5].x, o[5].y), pack2(o[6].x, o[6].y), pack2(o[7].x, o[7].y));
+                if (tile) {
+                    const int q = 4 * half + 2 * z;
+                    *reinterpret_cast<uint4 *>(vt + ((q ^ (row & 7)) << 4)) = r0;
+                    *reinterpret_cast<uint4 *>(vt + (((q + 1) ^ (row & 7)) << 4)) = r1;
+                } else if (row < n) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(w.o) + at) + 2 * z;
+                    if (nq > 2 * z) dst[0] = r0;
+                    if (nq > 2 * z + 1) dst[1] = r1;
                 }
             }
-        }
-    } else if (warp >= 12 && warp < 16) {
-        float S[64];
-        const bool live = row < w.da;
-        const float *src = STATE && A.nseg > 1 ? nullptr   // a segment's own sum
-                         : A.nseg > 1 ? A.seg[wi] + ((long long)sg * BH + bh) * w.da * w.dc
-                         : w.s_in ? w.s_in + (long long)bh * w.da * w.dc : nullptr;
-        const int sta = A.nseg > 1 ? w.dc : w.st_a, stc = A.nseg > 1 ? 1 : w.st_c;
-        const long long at = (long long)row * sta + (long long)c0 * stc;
-        const int cols = live ? w.dc - c0 : 0;
-        {
-            const float *q = src + at;
-            const int n = src ? cols : 0;
-#pragma unroll
-            for (int j = 0; j < 64; ++j, q += stc) S[j] = j < n ? *q : 0.f;
-        }
-        auto operand = [&]() {   // S in bf16, the layout of a V tile
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const uint4 v = make_uint4(pack2(S[8 * q], S[8 * q + 1]), pack2(S[8 * q + 2], S[8 * q + 3]),
-                                           pack2(S[8 * q + 4], S[8 * q + 5]), pack2(S[8 * q + 6], S[8 * q + 7]));
-                *reinterpret_cast<uint4 *>(sm + SM_S + row * 128 + ((q ^ (row & 7)) << 4)) = v;
-            }
-            fence_proxy_async();
-            warp_arrive(&B->s);
-        };
-        if (!STATE) operand();
-#pragma unroll 1
-        for (int c = 0; c < nch; ++c) {
-            const float E = f32[F_PW + ntok(chunk(c))];
-            if (!await_warp(B, &B->kv, (uint32_t)c)) break;
-            fence_after_sync();
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                uint32_t x[8], y[8], z[8];
-                tmem_ld8(tm + TM_KV + lane_q + 8u * q, x);
-                tmem_ld8(tm + TM_KV + lane_q + 64u + 8u * q, y);
-                tmem_ld8(tm + TM_KV + lane_q + 128u + 8u * q, z);
-                tmem_wait_ld8(x, y, z);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    S[8 * q + j] = fmaf(E, S[8 * q + j],
-                                        __uint_as_float(x[j]) + (__uint_as_float(y[j]) + __uint_as_float(z[j])));
-            }
             fence_before_sync();
-            warp_arrive(&B->kv_read);
-            if (!STATE && c + 1 < nch) {
-                // A S of this chunk has read the operand
-                if (!await_warp(B, &B->a_free[c & 1], (uint32_t)c >> 1)) break;
-                operand();
-            }
-        }
-        float *dst = A.nseg > 1 ? (STATE ? A.seg[wi] + ((long long)sg * BH + bh) * w.da * w.dc : nullptr)
-                                : w.s_out ? w.s_out + (long long)bh * w.da * w.dc : nullptr;
-        if (dst) {
-            float *q = dst + at;
-#pragma unroll
-            for (int j = 0; j < 64; ++j, q += stc)
-                if (j < cols) *q = S[j];
+            warp_arrive(&B->o_read);
+            fence_proxy_async();
+            warp_arrive(&B->o_tile);
         }
     } else if (warp >= 16) {
         const int t = tid - 512;
+        const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll 1
         for (int c = 0; c < nch; ++c) {
             unsigned char *st = sm + (c & 1) * STAGE;
             const int t0 = chunk(c), n = ntok(t0);
-            const bool fix = dirty(t0, n);
+            const bool fix = n < C && t0 + n < p.L;   // rows of other tokens (TMA fills those past L with zeros)
             if (!await_warp(B, &B->v_full[c & 1], (uint32_t)c >> 1)) break;
-            if (c > 0 && !await_warp(B, &B->kv, (uint32_t)c - 1u)) break;   // V' has been read
             if (fix && !await_warp(B, &B->k_full[c & 1], (uint32_t)c >> 1)) break;
             if (fix && !STATE && !await_warp(B, &B->sc, (uint32_t)c)) break;   // the scores have read K
+            bool ok = true;
 #pragma unroll 1
             for (int q = 0; q < 8; ++q) {
+                const int z = q >> 2;
+                if (q == 4 * z && c > 0 && !(ok = await_warp(B, &B->kv[z], (uint32_t)c - 1u))) break;   // this half has been read
                 const int ch = t + 128 * q, r = ch >> 3;   // 16-byte piece of row r
                 const uint32_t off = (uint32_t)ch * 16u;
                 uint4 x = *reinterpret_cast<const uint4 *>(st + ST_V + off);
@@ -537,32 +542,144 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
                     *reinterpret_cast<uint4 *>(st + ST_K + off) = x;
                     *reinterpret_cast<uint4 *>(st + ST_K + TILE + off) = x;
                 }
-                const float f = w.write * f32[F_PW + (rev ? r + 1 : max(0, n - 1 - r))];
+                const float f = w.write * f32[F_PW + (REV ? r + 1 : max(0, n - 1 - r))];
+                const float2 ff = make_float2(f, f);
                 const uint32_t u[4] = {x.x, x.y, x.z, x.w};
                 uint32_t o[3][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float a = lo_f(u[i]) * f, bb = hi_f(u[i]) * f;
+                    float2 a = mul2(make_float2(lo_f(u[i]), hi_f(u[i])), ff);
 #pragma unroll
-                    for (int z = 0; z < 3; ++z) {
-                        o[z][i] = high2(a, bb);
-                        a -= hi_f(__float_as_uint(a));
-                        bb -= hi_f(__float_as_uint(bb));
+                    for (int k = 0; k < 3; ++k) {
+                        o[k][i] = high2(a.x, a.y);
+                        a = fma2(make_float2(hi_f(__float_as_uint(a.x)), hi_f(__float_as_uint(a.y))), minus, a);
                     }
                 }
 #pragma unroll
-                for (int z = 0; z < 3; ++z)
-                    *reinterpret_cast<uint4 *>(sm + SM_VP + z * TILE + off) = make_uint4(o[z][0], o[z][1], o[z][2], o[z][3]);
+                for (int k = 0; k < 3; ++k)
+                    *reinterpret_cast<uint4 *>(sm + SM_VP + k * TILE + off) = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+                if ((q & 3) == 3) {
+                    fence_proxy_async();
+                    warp_arrive(&B->vp[z]);
+                }
             }
-            fence_proxy_async();
-            warp_arrive(&B->vp);
+            if (!ok) break;
+        }
+    } else if (warp >= 12) {
+        float2 S[32];
+        const bool seg = A.nseg > 1;
+        // where the state comes from and goes to: the caller's, or the segment's slot (a segment
+        // that only adds starts from zero; the states that leave are k_la_segments' work)
+        float *slot = seg ? A.seg[wi] + ((long long)sg * BH + bh) * w.da * w.dc : nullptr;
+        const long long outside = (long long)bh * w.da * w.dc;
+        const float *src = seg ? (STATE ? nullptr : slot) : w.s_in ? w.s_in + outside : nullptr;
+        float *dst = seg ? (STATE ? slot : nullptr) : w.s_out ? w.s_out + outside : nullptr;
+        const int stc = seg ? 1 : w.st_c, cols = row < w.da ? w.dc - c0 : 0;
+        const long long at = (long long)row * (seg ? w.dc : w.st_a) + (long long)c0 * stc;
+        // eight columns at a time through the last eight registers, the others moving down: rolled
+        // loops, so that what runs once does not crowd out the code of the chunks
+        auto turn = [&]() {
+#pragma unroll
+            for (int j = 0; j < 28; ++j) S[j] = S[j + 4];
+        };
+        const int got = src ? cols : 0;
+#pragma unroll 1
+        for (int j = 0; j < 64; j += 8) {
+            turn();
+            const float *q = src + at + j * stc;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                S[28 + i].x = j + 2 * i < got ? q[2 * i * stc] : 0.f;
+                S[28 + i].y = j + 2 * i + 1 < got ? q[(2 * i + 1) * stc] : 0.f;
+            }
+        }
+#pragma unroll 1
+        for (int c = 0; c < nch; ++c) {
+            if (!STATE) {   // S in bf16, the layout of a V tile; A S of the chunk before has read it
+                if (c > 0 && !await_warp(B, &B->a_free[(c - 1) & 1], (uint32_t)(c - 1) >> 1)) break;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const uint4 v = make_uint4(pack2(S[4 * q].x, S[4 * q].y), pack2(S[4 * q + 1].x, S[4 * q + 1].y),
+                                               pack2(S[4 * q + 2].x, S[4 * q + 2].y), pack2(S[4 * q + 3].x, S[4 * q + 3].y));
+                    *reinterpret_cast<uint4 *>(sm + SM_S + row * 128 + ((q ^ (row & 7)) << 4)) = v;
+                }
+                fence_proxy_async();
+                warp_arrive(&B->s);
+            }
+            const float E = f32[F_PW + ntok(chunk(c))];
+            const float2 EE = make_float2(E, E);
+            const uint32_t tk = tm + TM_KV + lane_q;
+            if (!await_warp(B, &B->kv[1], (uint32_t)c)) break;
+            fence_after_sync();
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                uint32_t x[8], y[8];
+                tmem_get8x2(tk + 64u + 8u * q, tk + 128u + 8u * q, x, y);
+                float2 small[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) small[k] = add2(asf2(x[2 * k], x[2 * k + 1]), asf2(y[2 * k], y[2 * k + 1]));
+                tmem_get8(tk + 8u * q, x);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    S[4 * q + k] = fma2(EE, S[4 * q + k], add2(asf2(x[2 * k], x[2 * k + 1]), small[k]));
+            }
+            fence_before_sync();
+            warp_arrive(&B->kv_read);
+        }
+        if (dst) {
+#pragma unroll 1
+            for (int j = 0; j < 64; j += 8) {
+                float *q = dst + at + j * stc;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (j + 2 * i < cols) q[2 * i * stc] = S[i].x;
+                    if (j + 2 * i + 1 < cols) q[(2 * i + 1) * stc] = S[i].y;
+                }
+                turn();
+            }
         }
     }
+}
+
+template <bool STATE>
+__global__ void __launch_bounds__(THREADS, 1)
+k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
+          const __grid_constant__ Maps m2, const __grid_constant__ Args A) {
+    const int BH = A.p.B * A.p.H;
+    int id = blockIdx.x;
+    const int slice = id % A.slices;
+    id /= A.slices;
+    const int bh = id % BH;
+    id /= BH;
+    const int sg = id % A.nseg, wi = id / A.nseg;
+    const LaWalk &w = A.p.w[wi];
+    const Maps &maps = wi == 0 ? m0 : wi == 1 ? m1 : m2;
+    if (64 * slice >= w.dc) return;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars *B = reinterpret_cast<Bars *>(sm + SM_BAR);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i)
+            for (uint64_t *q : {&B->a_full[i], &B->k_full[i], &B->v_full[i], &B->a_free[i], &B->k_free[i], &B->v_free[i]})
+                mbar_init(q, 1);
+        for (uint64_t *q : {&B->sc, &B->kv[0], &B->kv[1], &B->o, &B->end}) mbar_init(q, 1);
+        // an arrival a warp
+        for (uint64_t *q : {&B->vp[0], &B->vp[1], &B->s, &B->kv_read}) mbar_init(q, 4);
+        for (uint64_t *q : {&B->p, &B->sc_read, &B->o_read, &B->o_tile}) mbar_init(q, 8);
+        B->abort = 0;
+        mbar_fence_init();
+    }
+    if (threadIdx.x / 32 == 1) tmem_alloc(&B->tslot, TM_COLS);
+    if (STATE || !w.o_f32)
+        w.rev ? walk<STATE, true, 0>(A, maps, w, wi, slice, bh, sg, sm) : walk<STATE, false, 0>(A, maps, w, wi, slice, bh, sg, sm);
+    else
+        w.rev ? walk<STATE, true, 1>(A, maps, w, wi, slice, bh, sg, sm) : walk<STATE, false, 1>(A, maps, w, wi, slice, bh, sg, sm);
     fence_before_sync();
     __syncthreads();
-    if (warp == 1) {
+    if (threadIdx.x / 32 == 1) {
         fence_after_sync();
-        tmem_dealloc(tm, TM_COLS);
+        tmem_dealloc(B->tslot, TM_COLS);
     }
 }
 
@@ -655,6 +772,8 @@ bool la_chunked(const LaArgs &p, int nseg, float *const *seg, cudaStream_t st, c
         if (!la_chunked_sizes(p.bf16, w.da, w.dc) || !ok(w.a, w.sa, 8) || !ok(w.k, w.sk, 8) ||
             !ok(w.v, w.sv, 8) || (w.o && !ok(w.o, w.so, w.o_f32 ? 4 : 8)))
             return false;
+        m[i].o = CUtensorMap{};
+        if (w.o && !w.o_f32 && !make_map(&m[i].o, w.o, w.dc, p.H, p, w.so)) return false;
         if (!make_map(&m[i].a, w.a, w.da, p.H / w.rep_a, p, w.sa) ||
             !make_map(&m[i].k, w.k, w.da, p.H / w.rep_k, p, w.sk) ||
             !make_map(&m[i].v, w.v, w.dc, p.H / w.rep_v, p, w.sv))
@@ -662,7 +781,6 @@ bool la_chunked(const LaArgs &p, int nseg, float *const *seg, cudaStream_t st, c
         const int sl = (w.dc + 63) / 64;
         A.slices = sl > A.slices ? sl : A.slices;
         A.seg[i] = seg[i];
-        A.o32[i] = w.o && !w.o_f32 && ((uintptr_t)w.o & 31) == 0 && w.so[0] % 16 == 0 && w.so[1] % 16 == 0 && w.so[2] % 16 == 0;
     }
     const int nc = (p.L + C - 1) / C;
     A.G = (nc + nseg - 1) / nseg;
