@@ -20,7 +20,7 @@
 //     warp 2       TMA stores of the output, which is laid over the chunk's V tile
 //     warps 4-11   P from the scores, and the output (a thread a token and half of the columns)
 //     warps 12-15  the state (a thread a state row, 64 values in registers)
-//     warps 16-19  V', in halves of 64 tokens
+//     warps 16-19  V', in halves of 64 tokens, v straight from L2
 // so that P is made while K^T V' and A S run, and V', the state and the output of one chunk
 // beside the products of the next.  Every role runs its own code once a chunk, so the walk is
 // compiled for each direction and kind of output and its loops stay rolled: instruction fetch
@@ -229,20 +229,23 @@ __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// (`last`: a wait for what is in flight when the block ends, whatever the others do)
-__device__ __noinline__ bool poll_on(Bars *B, uint32_t bar, uint32_t parity, bool last) {
+__device__ __forceinline__ bool await(Bars *B, uint64_t *bar, uint32_t n) {
+    const uint32_t a = smem_u32(bar);
 #pragma unroll 1
     for (uint32_t i = 0; i < POLLS; ++i) {
-        if (poll(bar, parity)) return true;
-        if (!last && *reinterpret_cast<volatile int *>(&B->abort)) return false;
+        if (poll(a, n & 1u)) return true;
+        if (*reinterpret_cast<volatile int *>(&B->abort)) return false;
     }
     *reinterpret_cast<volatile int *>(&B->abort) = 1;
     atomicCAS(&ssm_la_error_word, 0, 1);
     return false;
 }
-__device__ __forceinline__ bool await(Bars *B, uint64_t *bar, uint32_t n) {
+// A wait for what is in flight when the block ends, whatever the others do.
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t n) {
     const uint32_t a = smem_u32(bar);
-    return poll(a, n & 1u) || poll_on(B, a, n & 1u, false);
+#pragma unroll 1
+    for (uint32_t i = 0; i < POLLS && !poll(a, n & 1u); ++i) {
+    }
 }
 // The same for a whole warp, all lanes alike.
 __device__ __forceinline__ bool await_warp(Bars *B, uint64_t *bar, uint32_t n) {
@@ -318,17 +321,19 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                         tma_load_4d(st + ST_A + i * TILE, &maps.a, &B->a_full[s], 64 * i, ha, t0, b);
                     ++got_a;
                 }
-                if (c >= 2 && !await(B, &B->v_free[s], n)) break;
-                mbar_expect_tx(&B->v_full[s], TILE);
-                tma_load_4d(st + ST_V, &maps.v, &B->v_full[s], c0, hv, t0, b);
-                ++got_v;
+                if (!STATE) {
+                    if (c >= 2 && !await(B, &B->v_free[s], n)) break;
+                    mbar_expect_tx(&B->v_full[s], TILE);
+                    tma_load_4d(st + ST_V, &maps.v, &B->v_full[s], c0, hv, t0, b);
+                    ++got_v;
+                }
             }
             // no copy is in flight when the block ends
 #pragma unroll 1
             for (uint32_t i = 0; i < 6; ++i) {
                 const uint32_t got = i < 2 ? got_a : i < 4 ? got_k : got_v, back = 1 + (i & 1);
                 uint64_t *full = i < 2 ? B->a_full : i < 4 ? B->k_full : B->v_full;
-                if (got >= back) poll_on(B, smem_u32(&full[(got - back) & 1]), ((got - back) >> 1) & 1u, true);
+                if (got >= back) drain(&full[(got - back) & 1], (got - back) >> 1);
             }
         }
         __syncwarp();
@@ -384,7 +389,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                 if (!STATE) {
                     if (c + 1 < nch && !scores(c + 1)) break;
                     if (c >= 0) {
-                        if (!await(B, &B->p, (uint32_t)c)) break;
+                        if (!await(B, &B->v_full[c & 1], (uint32_t)c >> 1) || !await(B, &B->p, (uint32_t)c)) break;
                         fence_after_sync();
 #pragma unroll 1
                         for (int s = 0; s < 8; ++s)
@@ -392,10 +397,9 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                         mma_commit(&B->o);
                     }
                 }
-                if (STATE) mma_commit(&B->v_free[c & 1]);   // else warp 2, when the output has left it
             }
             mma_commit(&B->end);   // every MMA is over before tensor memory goes
-            poll_on(B, smem_u32(&B->end), 0u, true);
+            drain(&B->end, 0u);
         }
         __syncwarp();
     } else if (!STATE && warp == 2) {
@@ -518,52 +522,69 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             warp_arrive(&B->o_tile);
         }
     } else if (warp >= 16) {
-        const int t = tid - 512;
+        // V' = write lam^.. v, from memory by way of registers half a chunk ahead: it does not wait
+        // for a free V tile, nor hold one.  A thread takes 8 columns of four rows of each half.
+        const int t = tid - 512, col = 8 * (t & 7);
         const float2 minus = make_float2(-1.f, -1.f);
+        const __nv_bfloat16 *vg = reinterpret_cast<const __nv_bfloat16 *>(w.v) + b * w.sv[0] + (h / w.rep_v) * w.sv[2] + c0 + col;
+        const bool mine = c0 + col < w.dc;
+        uint4 cur[4], nxt[4];
+        auto fetch = [&](int hh) {   // rows of half hh & 1 of chunk hh >> 1
+            const int t0 = chunk(hh >> 1), n = ntok(t0), r0 = (t >> 3) + 64 * (hh & 1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                nxt[i] = mine && r0 + 16 * i < n ? *reinterpret_cast<const uint4 *>(vg + (long long)(t0 + r0 + 16 * i) * w.sv[1])
+                                                 : make_uint4(0u, 0u, 0u, 0u);
+        };
+        if (nch > 0) fetch(0);
 #pragma unroll 1
-        for (int c = 0; c < nch; ++c) {
+        for (int hh = 0; hh < 2 * nch; ++hh) {
+            const int c = hh >> 1, z = hh & 1;
             unsigned char *st = sm + (c & 1) * STAGE;
             const int t0 = chunk(c), n = ntok(t0);
             const bool fix = n < C && t0 + n < p.L;   // rows of other tokens (TMA fills those past L with zeros)
-            if (!await_warp(B, &B->v_full[c & 1], (uint32_t)c >> 1)) break;
-            if (fix && !await_warp(B, &B->k_full[c & 1], (uint32_t)c >> 1)) break;
-            if (fix && !STATE && !await_warp(B, &B->sc, (uint32_t)c)) break;   // the scores have read K
-            bool ok = true;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
+            if (hh + 1 < 2 * nch) fetch(hh + 1);
+            if (fix) {   // the scores have read K
+                if (!await_warp(B, &B->k_full[c & 1], (uint32_t)c >> 1)) break;
+                if (!STATE && !await_warp(B, &B->v_full[c & 1], (uint32_t)c >> 1)) break;
+                if (!STATE && !await_warp(B, &B->sc, (uint32_t)c)) break;
+            }
+            if (c > 0 && !await_warp(B, &B->kv[z], (uint32_t)c - 1u)) break;   // this half has been read
 #pragma unroll 1
-            for (int q = 0; q < 8; ++q) {
-                const int z = q >> 2;
-                if (q == 4 * z && c > 0 && !(ok = await_warp(B, &B->kv[z], (uint32_t)c - 1u))) break;   // this half has been read
-                const int ch = t + 128 * q, r = ch >> 3;   // 16-byte piece of row r
-                const uint32_t off = (uint32_t)ch * 16u;
-                uint4 x = *reinterpret_cast<const uint4 *>(st + ST_V + off);
+            for (int i = 0; i < 4; ++i) {
+                const int r = (t >> 3) + 64 * z + 16 * i;
+                const uint32_t off = (uint32_t)r * 128u + (uint32_t)((col / 8) ^ (r & 7)) * 16u;
+                const uint4 x = cur[0];
+                cur[0] = cur[1];
+                cur[1] = cur[2];
+                cur[2] = cur[3];
                 if (fix && r >= n) {
-                    x = make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4 *>(st + ST_V + off) = x;
-                    *reinterpret_cast<uint4 *>(st + ST_K + off) = x;
-                    *reinterpret_cast<uint4 *>(st + ST_K + TILE + off) = x;
+                    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                    if (!STATE) *reinterpret_cast<uint4 *>(st + ST_V + off) = zero;
+                    *reinterpret_cast<uint4 *>(st + ST_K + off) = zero;
+                    *reinterpret_cast<uint4 *>(st + ST_K + TILE + off) = zero;
                 }
                 const float f = w.write * f32[F_PW + (REV ? r + 1 : max(0, n - 1 - r))];
                 const float2 ff = make_float2(f, f);
                 const uint32_t u[4] = {x.x, x.y, x.z, x.w};
                 uint32_t o[3][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float2 a = mul2(make_float2(lo_f(u[i]), hi_f(u[i])), ff);
+                for (int k = 0; k < 4; ++k) {
+                    float2 a = mul2(make_float2(lo_f(u[k]), hi_f(u[k])), ff);
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        o[k][i] = high2(a.x, a.y);
+                    for (int q = 0; q < 3; ++q) {
+                        o[q][k] = high2(a.x, a.y);
                         a = fma2(make_float2(hi_f(__float_as_uint(a.x)), hi_f(__float_as_uint(a.y))), minus, a);
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    *reinterpret_cast<uint4 *>(sm + SM_VP + k * TILE + off) = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
-                if ((q & 3) == 3) {
-                    fence_proxy_async();
-                    warp_arrive(&B->vp[z]);
-                }
+                for (int q = 0; q < 3; ++q)
+                    *reinterpret_cast<uint4 *>(sm + SM_VP + q * TILE + off) = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
             }
-            if (!ok) break;
+            fence_proxy_async();
+            warp_arrive(&B->vp[z]);
         }
     } else if (warp >= 12) {
         float2 S[32];
