@@ -344,45 +344,54 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             constexpr uint32_t id_kv = idesc_bf16(128, 192, true, true);
             // descriptors: their address field counts 16-byte units; along a row, 16 values are 2 of them
             const uint32_t u0 = base >> 4;
-            auto kmaj = [&](uint32_t tile, int s) { return desc<16u>(u0 + (tile >> 4) + (s >> 2) * (TILE >> 4) + (s & 3) * 2u); };
-            auto mnmaj = [&](uint32_t tile, int s) { return desc<TILE>(u0 + (tile >> 4) + 128u * s); };
             const int ks = (w.da + 15) / 16;
+            constexpr uint32_t HALF = TILE >> 4, STEP = 2048 >> 4;   // the next 64 values of the rows; the next 16 rows
+            // a chunk's products over the head dimension, for whole heads of 128 without a loop: the
+            // thread that issues is on the critical path, and a rolled loop takes it 130 cycles an MMA
+            auto over_head = [&](uint32_t d, uint32_t a, uint32_t bb, uint32_t id, auto desc_b) {
+                if (ks == 8) {
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) mma_bf16(d, desc<16u>(a + (s >> 2) * HALF + (s & 3) * 2u), desc_b(bb, s), id, s > 0);
+                } else {
+#pragma unroll 1
+                    for (int s = 0; s < ks; ++s) mma_bf16(d, desc<16u>(a + (s >> 2) * HALF + (s & 3) * 2u), desc_b(bb, s), id, s > 0);
+                }
+            };
+            auto kmaj = [](uint32_t u, int s) { return desc<16u>(u + (s >> 2) * HALF + (s & 3) * 2u); };
+            auto mnmaj = [](uint32_t u, int s) { return desc<TILE>(u + STEP * s); };
             auto scores = [&](int c) {
-                const uint32_t st = (c & 1) ? STAGE : 0u;
+                const uint32_t st = u0 + ((c & 1) ? STAGE >> 4 : 0u);
                 if (!await(B, &B->k_full[c & 1], (uint32_t)c >> 1) || !await(B, &B->a_full[c & 1], (uint32_t)c >> 1)) return false;
                 if (c > 0 && !await(B, &B->sc_read, (uint32_t)c - 1u)) return false;
                 fence_after_sync();
-#pragma unroll 1
-                for (int s = 0; s < ks; ++s)
-                    mma_bf16(tm + TM_SC, kmaj(st + ST_A, s), kmaj(st + ST_K, s), id_sc, s > 0);
+                over_head(tm + TM_SC, st + (ST_A >> 4), st + (ST_K >> 4), id_sc, kmaj);
                 mma_commit(&B->sc);
                 return true;
             };
-            bool ok = true;
 #pragma unroll 1
             for (int c = STATE ? 0 : -1; c < nch; ++c) {
-                const uint32_t st = (c & 1) ? STAGE : 0u;
+                const uint32_t st = u0 + ((c & 1) ? STAGE >> 4 : 0u);
                 if (c >= 0) {
                     if (STATE && !await(B, &B->k_full[c & 1], (uint32_t)c >> 1)) break;
                     if (c > 0 && !await(B, &B->kv_read, (uint32_t)c - 1u)) break;
-#pragma unroll 1
-                    for (int z = 0; z < 2; ++z) {
-                        if (!(ok = await(B, &B->vp[z], (uint32_t)c))) break;
-                        fence_after_sync();
-#pragma unroll 1
-                        for (int s = 0; s < 4; ++s)
-                            mma_bf16(tm + TM_KV, mnmaj(st + ST_K, 4 * z + s), mnmaj(SM_VP, 4 * z + s), id_kv, z > 0 || s > 0);
-                        mma_commit(&B->kv[z]);
-                    }
-                    if (!ok) break;
+                    if (!await(B, &B->vp[0], (uint32_t)c)) break;
+                    fence_after_sync();
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        mma_bf16(tm + TM_KV, mnmaj(st + (ST_K >> 4), s), mnmaj(u0 + (SM_VP >> 4), s), id_kv, s > 0);
+                    mma_commit(&B->kv[0]);
+                    if (!await(B, &B->vp[1], (uint32_t)c)) break;
+                    fence_after_sync();
+#pragma unroll
+                    for (int s = 4; s < 8; ++s)
+                        mma_bf16(tm + TM_KV, mnmaj(st + (ST_K >> 4), s), mnmaj(u0 + (SM_VP >> 4), s), id_kv, true);
+                    mma_commit(&B->kv[1]);
                     mma_commit(&B->k_free[c & 1]);
                     if (!STATE) {
                         if (!await(B, &B->s, (uint32_t)c)) break;
                         if (c > 0 && !await(B, &B->o_read, (uint32_t)c - 1u)) break;
                         fence_after_sync();
-#pragma unroll 1
-                        for (int s = 0; s < ks; ++s)
-                            mma_bf16(tm + TM_OS, kmaj(st + ST_A, s), mnmaj(SM_S, s), id_n, s > 0);
+                        over_head(tm + TM_OS, st + (ST_A >> 4), u0 + (SM_S >> 4), id_n, mnmaj);
                         mma_commit(&B->a_free[c & 1]);
                     }
                 }
@@ -391,9 +400,9 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                     if (c >= 0) {
                         if (!await(B, &B->v_full[c & 1], (uint32_t)c >> 1) || !await(B, &B->p, (uint32_t)c)) break;
                         fence_after_sync();
-#pragma unroll 1
+#pragma unroll
                         for (int s = 0; s < 8; ++s)
-                            mma_bf16_ts(tm + TM_OI, tm + TM_P + 8u * s, mnmaj(st + ST_V, s), id_n, s > 0);
+                            mma_bf16_ts(tm + TM_OI, tm + TM_P + 8u * s, mnmaj(st + (ST_V >> 4), s), id_n, s > 0);
                         mma_commit(&B->o);
                     }
                 }
