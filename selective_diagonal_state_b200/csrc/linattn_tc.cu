@@ -81,6 +81,14 @@ template <uint32_t LBO> __device__ __forceinline__ uint64_t desc(uint32_t units)
     constexpr uint32_t hi = (1024u >> 4) | 1u << 14 | LAYOUT_SW128 << 29;
     return (uint64_t)hi << 32 | (units | (LBO >> 4) << 16);
 }
+// 16 bytes that stay out of L1
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
 // Prefetch of a tile into L2.
 __device__ __forceinline__ void tma_prefetch_4d(const void *tmap, int c0, int c1, int c2, int c3) {
     asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];\n" ::"l"(
@@ -542,8 +550,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             const int t0 = chunk(hh >> 1), n = ntok(t0), r0 = (t >> 3) + 64 * (hh & 1);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                nxt[i] = mine && r0 + 16 * i < n ? *reinterpret_cast<const uint4 *>(vg + (long long)(t0 + r0 + 16 * i) * w.sv[1])
-                                                 : make_uint4(0u, 0u, 0u, 0u);
+                nxt[i] = mine && r0 + 16 * i < n ? ld_once(vg + (long long)(t0 + r0 + 16 * i) * w.sv[1]) : make_uint4(0u, 0u, 0u, 0u);
         };
         if (nch > 0) fetch(0);
 #pragma unroll 1
