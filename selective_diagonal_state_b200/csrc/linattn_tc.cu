@@ -17,7 +17,7 @@
 // chunk 80 KB come in by TMA and 16 KB go out.  One block an SM, its 20 warps with a role each:
 //     warp 0       TMA loads, two chunks ahead, each tile again as soon as its last reader is done
 //     warp 1       all MMAs, per chunk: K^T V', A S, the next chunk's A K^T, P V
-//     warp 2       TMA stores of the output, which is laid over the chunk's V tile
+//     warp 2       TMA stores of the output, which is laid over the chunk's V tile (fp32: A tiles)
 //     warps 4-11   P from the scores, and the output (a thread a token and half of the columns)
 //     warps 12-15  the state (a thread a state row, 64 values in registers)
 //     warps 16-19  V', in halves of 64 tokens, v straight from L2
@@ -211,7 +211,7 @@ __device__ __forceinline__ float2 asf2(uint32_t a, uint32_t b) { return make_flo
 struct Bars {
     uint64_t a_full[2], k_full[2], v_full[2];   // tiles loaded
     uint64_t a_free[2], k_free[2], v_free[2];   // tiles read by their last product
-    uint64_t sc, kv[2], o;                      // products done: scores; K^T V' (halves of the tokens); A S and P V
+    uint64_t sc, kv[2], as, o;                  // products done: scores; K^T V' (halves of the tokens); A S; P V
     uint64_t p, vp[2], s;                       // operands written: P, V' (halves), S
     uint64_t sc_read, kv_read, o_read;          // results fetched from tensor memory
     uint64_t o_tile;                            // the output in shared memory, or stored
@@ -400,7 +400,8 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                         if (c > 0 && !await(B, &B->o_read, (uint32_t)c - 1u)) break;
                         fence_after_sync();
                         over_head(tm + TM_OS, st + (ST_A >> 4), u0 + (SM_S >> 4), id_n, mnmaj);
-                        mma_commit(&B->a_free[c & 1]);
+                        mma_commit(&B->as);
+                        if (OUT == 0) mma_commit(&B->a_free[c & 1]);   // else warp 2, when the output has left the tile
                     }
                 }
                 if (!STATE) {
@@ -412,6 +413,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                         for (int s = 0; s < 8; ++s)
                             mma_bf16_ts(tm + TM_OI, tm + TM_P + 8u * s, mnmaj(st + (ST_V >> 4), s), id_n, s > 0);
                         mma_commit(&B->o);
+                        if (OUT == 1) mma_commit(&B->v_free[c & 1]);
                     }
                 }
             }
@@ -425,12 +427,17 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             for (int c = 0; c < nch; ++c) {
                 const int t0 = chunk(c), n = ntok(t0);
                 if (!await(B, &B->o_tile, (uint32_t)c)) break;
-                if (OUT == 0 && !(n < C && t0 + n < p.L)) {   // what is past L or the head is not written
+                // what is past L or the head is not written
+                if (OUT == 1) {   // (rows behind the sequence hold nothing that is read)
+                    const unsigned char *at = sm + (c & 1) * STAGE + ST_A;
+                    tma_store_4d(&maps.o, at, c0, h, t0, b);
+                    if (c0 + 32 < w.dc) tma_store_4d(&maps.o, at + TILE, c0 + 32, h, t0, b);
+                } else if (!(n < C && t0 + n < p.L)) {
                     tma_store_4d(&maps.o, sm + (c & 1) * STAGE + ST_V, c0, h, t0, b);
-                    bulk_commit();
-                    bulk_wait_read_all();
                 }
-                mbar_arrive(&B->v_free[c & 1]);
+                bulk_commit();
+                bulk_wait_read_all();
+                mbar_arrive(OUT == 1 ? &B->a_free[c & 1] : &B->v_free[c & 1]);
             }
             bulk_wait_all();
         }
@@ -500,10 +507,11 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             fence_after_sync();
             const float e = w.read * f32[F_PW + max(0, REV ? n - 1 - row : row + 1)];
             const float2 ee = make_float2(e, e);
-            // 16 columns at a time: over the chunk's V tile, from where warp 2 stores whole chunks, or,
-            // where rows behind the sequence must stay as they are, straight to memory
+            // 16 columns at a time: over the chunk's V tile (fp32: its A tiles), from where warp 2 stores
+            // whole chunks, or, where rows behind the sequence must stay as they are, straight to memory
             const bool tile = OUT == 0 && !(n < C && t0 + n < p.L);
             unsigned char *vt = sm + (c & 1) * STAGE + ST_V + row * 128;
+            unsigned char *at32 = sm + (c & 1) * STAGE + ST_A + half * TILE + row * 128;
             const long long at = ob + (long long)(t0 + row) * w.so[1];
 #pragma unroll 1
             for (int z = 0; z < 2; ++z) {
@@ -513,12 +521,10 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] = fma2(ee, asf2(u[2 * j], u[2 * j + 1]), asf2(x[2 * j], x[2 * j + 1]));
                 if (OUT == 1) {
-                    if (row < n) {
-                        float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(w.o) + at) + 4 * z;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (q < 2 * nq - 4 * z) dst[q] = make_float4(o[2 * q].x, o[2 * q].y, o[2 * q + 1].x, o[2 * q + 1].y);
-                    }
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<float4 *>(at32 + (((4 * z + q) ^ (row & 7)) << 4)) =
+                            make_float4(o[2 * q].x, o[2 * q].y, o[2 * q + 1].x, o[2 * q + 1].y);
                     continue;
                 }
                 const uint4 r0 = make_uint4(pack2(o[0].x, o[0].y), pack2(o[1].x, o[1].y), pack2(o[2].x, o[2].y), pack2(o[3].x, o[3].y));
@@ -633,7 +639,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
 #pragma unroll 1
         for (int c = 0; c < nch; ++c) {
             if (!STATE) {   // S in bf16, the layout of a V tile; A S of the chunk before has read it
-                if (c > 0 && !await_warp(B, &B->a_free[(c - 1) & 1], (uint32_t)(c - 1) >> 1)) break;
+                if (c > 0 && !await_warp(B, &B->as, (uint32_t)c - 1u)) break;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     const uint4 v = make_uint4(pack2(S[4 * q].x, S[4 * q].y), pack2(S[4 * q + 1].x, S[4 * q + 1].y),
@@ -700,7 +706,7 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
         for (int i = 0; i < 2; ++i)
             for (uint64_t *q : {&B->a_full[i], &B->k_full[i], &B->v_full[i], &B->a_free[i], &B->k_free[i], &B->v_free[i]})
                 mbar_init(q, 1);
-        for (uint64_t *q : {&B->sc, &B->kv[0], &B->kv[1], &B->o, &B->end}) mbar_init(q, 1);
+        for (uint64_t *q : {&B->sc, &B->kv[0], &B->kv[1], &B->as, &B->o, &B->end}) mbar_init(q, 1);
         // an arrival a warp
         for (uint64_t *q : {&B->vp[0], &B->vp[1], &B->s, &B->kv_read}) mbar_init(q, 4);
         for (uint64_t *q : {&B->p, &B->sc_read, &B->o_read, &B->o_tile}) mbar_init(q, 8);
@@ -744,15 +750,17 @@ __global__ void __launch_bounds__(256) k_la_segments(const __grid_constant__ Arg
     if (w.s_out) w.s_out[ext] = E;
 }
 
-bool make_map(CUtensorMap *m, const void *base, int d, int heads, const LaArgs &p, const long long *s) {
+// bf16, boxes of 64 values, or fp32, boxes of 32: 128 bytes either way
+bool make_map(CUtensorMap *m, const void *base, int d, int heads, const LaArgs &p, const long long *s, bool f32 = false) {
     chunkc::EncodeTiledFn fn = chunkc::encode_fn();
     if (!fn) return false;
     cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)p.L, (cuuint64_t)p.B};
     // the stride of a dimension of one is not used, and need not be a valid one
-    cuuint64_t st[3] = {(cuuint64_t)(heads > 1 ? s[2] * 2 : 16), (cuuint64_t)(p.L > 1 ? s[1] * 2 : 16),
-                        (cuuint64_t)(p.B > 1 ? s[0] * 2 : 16)};
-    cuuint32_t box[4] = {64, 1, C, 1}, es[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, st, box, es,
+    const int e = f32 ? 4 : 2;
+    cuuint64_t st[3] = {(cuuint64_t)(heads > 1 ? s[2] * e : 16), (cuuint64_t)(p.L > 1 ? s[1] * e : 16),
+                        (cuuint64_t)(p.B > 1 ? s[0] * e : 16)};
+    cuuint32_t box[4] = {(cuuint32_t)(128 / e), 1, C, 1}, es[4] = {1, 1, 1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, st, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -810,7 +818,7 @@ bool la_chunked(const LaArgs &p, int nseg, float *const *seg, cudaStream_t st, c
             !ok(w.v, w.sv, 8) || (w.o && !ok(w.o, w.so, w.o_f32 ? 4 : 8)))
             return false;
         m[i].o = CUtensorMap{};
-        if (w.o && !w.o_f32 && !make_map(&m[i].o, w.o, w.dc, p.H, p, w.so)) return false;
+        if (w.o && !make_map(&m[i].o, w.o, w.dc, p.H, p, w.so, w.o_f32)) return false;
         if (!make_map(&m[i].a, w.a, w.da, p.H / w.rep_a, p, w.sa) ||
             !make_map(&m[i].k, w.k, w.da, p.H / w.rep_k, p, w.sk) ||
             !make_map(&m[i].v, w.v, w.dc, p.H / w.rep_v, p, w.sv))
