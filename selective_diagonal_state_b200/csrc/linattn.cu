@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(256) k_la_recurrent(const LaArgs p, int slices
             sv[i][e & 31] = x * w.write;
         }
         __syncthreads();
+#pragma unroll 4
         for (int i = 0; i < m; ++i) {
             const float v = sv[i][lane];
             float o = 0.f;

@@ -2,10 +2,14 @@
 // gradient:
 //     r = x + residual,  rstd = (mean(r^2) + eps)^{-1/2},  y = r rstd w,
 //     dx = rstd (w dy - xhat mean(w dy xhat)) + dr,  xhat = r rstd,  dw = sum_rows dy xhat.
-// Bound by memory: a row is read once, kept in registers as it was loaded (16-byte
-// pieces, V of them a thread) while the team of T threads that holds it sums its squares,
-// and written once.  Sums are fp32.  r is rounded to the I/O type before its norm is
-// taken, so that the norm is that of the stored residual stream, which the backward reads.
+// Bound by memory: a row is read once, kept in registers (V 16-byte pieces a thread) while the
+// team of T threads that holds it sums its squares, and written once.  Sums are fp32.  r is
+// rounded to the I/O type before its norm is taken, so that the norm is that of the stored
+// residual stream, which the backward reads.
+//
+// With many rows a team is a warp (rows up to 2048 bf16 values): no barriers, and 8 x 16
+// bytes a lane and tensor in flight; with a block a row instead, 65536 x 2048 with a row scale took 206 us.
+// With few rows, a decoding step's, a block takes a row, for the shortest chain.
 #include <cuda_fp8.h>
 #include <float.h>
 
@@ -64,7 +68,7 @@ __device__ __forceinline__ uint16_t e4m3x2(float a, float b) {
 }
 
 // Team reduction: T threads (a power of two) of a block, consecutive; `buf` has a float a
-// warp.  Every thread of the block calls it.
+// warp.  Every thread of the team calls it.
 template <int T, bool MAX>
 __device__ __forceinline__ float team_reduce(float v, float *buf) {
 #pragma unroll
@@ -74,9 +78,10 @@ __device__ __forceinline__ float team_reduce(float v, float *buf) {
     }
     if constexpr (T > 32) {
         const int warp = threadIdx.x >> 5, first = warp & ~(T / 32 - 1);
-        __syncthreads();   // the buffer's last use is over
+        const int bar = 1 + threadIdx.x / T;   // the team's own barrier
+        asm volatile("bar.sync %0, %1;\n" ::"r"(bar), "n"(T) : "memory");   // the buffer's last use is over
         if ((threadIdx.x & 31) == 0) buf[warp] = v;
-        __syncthreads();
+        asm volatile("bar.sync %0, %1;\n" ::"r"(bar), "n"(T) : "memory");
         v = buf[first];
 #pragma unroll
         for (int i = 1; i < T / 32; ++i) v = MAX ? top(v, buf[first + i]) : v + buf[first + i];
@@ -95,8 +100,9 @@ struct FwdArgs {
     float eps;
 };
 
-template <bool BF16, int V, int T, int BLOCK>
-__global__ void __launch_bounds__(BLOCK) k_rmsnorm_fwd(const FwdArgs p) {
+template <bool BF16, int V, int T, int QUANT>
+__global__ void __launch_bounds__(T < 256 ? 256 : T) k_rmsnorm_fwd(const FwdArgs p) {
+    constexpr int BLOCK = T < 256 ? 256 : T;
     using I = Io<BF16>;
     constexpr int N = I::N, ES = 16 / N;
     __shared__ float buf[BLOCK / 32];
@@ -138,20 +144,18 @@ __global__ void __launch_bounds__(BLOCK) k_rmsnorm_fwd(const FwdArgs p) {
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) ss = fmaf(a[i], a[i], ss);
-    }
-    if (p.r) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int v = lane + k * T;
-            if (live && v < nv) *const_cast<uint4 *>(at(p.r, p.sr, v)) = raw[k];
-        }
+        const int v = lane + k * T;
+        if (p.r && live && v < nv) *const_cast<uint4 *>(at(p.r, p.sr, v)) = raw[k];
     }
     ss = team_reduce<T, false>(ss, buf);
     const float rstd = rsqrtf(ss / (float)p.dim + p.eps);
     if (p.rstd && live && lane == 0) p.rstd[row] = rstd;
+    // the norm of piece k, in fp32
     auto value = [&](int k, float *a) {
         const int v = lane + k * T;
         I::unpack(raw[k], a);
+#pragma unroll
+        for (int i = 0; i < N; ++i) a[i] *= rstd;
         if (p.w && v < nv) {
             float w[N];
 #pragma unroll
@@ -159,13 +163,10 @@ __global__ void __launch_bounds__(BLOCK) k_rmsnorm_fwd(const FwdArgs p) {
                 *reinterpret_cast<float4 *>(w + 4 * q) =
                     __ldg(reinterpret_cast<const float4 *>(p.w) + (long long)v * (N / 4) + q);
 #pragma unroll
-            for (int i = 0; i < N; ++i) a[i] = a[i] * rstd * w[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) a[i] *= rstd;
+            for (int i = 0; i < N; ++i) a[i] *= w[i];
         }
     };
-    if (p.y) {
+    if (QUANT == SSM_QUANT_NONE) {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int v = lane + k * T;
@@ -173,29 +174,30 @@ __global__ void __launch_bounds__(BLOCK) k_rmsnorm_fwd(const FwdArgs p) {
             value(k, a);
             if (live && v < nv) *const_cast<uint4 *>(at(p.y, p.sy, v)) = I::pack(a);
         }
+        return;
     }
-    if (!p.quant) return;
+    float y[V][N];
     float whole = 0.f;
-    if (p.quant == SSM_QUANT_ROW) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            float a[N];
-            value(k, a);
+    for (int k = 0; k < V; ++k) {
+        const int v = lane + k * T;
+        value(k, y[k]);
+        if (p.y && live && v < nv) *const_cast<uint4 *>(at(p.y, p.sy, v)) = I::pack(y[k]);
+        if (QUANT == SSM_QUANT_ROW)
 #pragma unroll
-            for (int i = 0; i < N; ++i) whole = top(whole, fabsf(a[i]));
-        }
+            for (int i = 0; i < N; ++i) whole = top(whole, fabsf(y[k][i]));
+    }
+    if (QUANT == SSM_QUANT_ROW) {
         whole = team_reduce<T, true>(whole, buf);
         if (live && lane == 0) p.scales[row] = whole / E4M3_MAX;
     }
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const int v = lane + k * T;
-        float a[N], m = whole;
-        value(k, a);
-        if (p.quant == SSM_QUANT_BLOCK) {   // 128 columns: 128 / N neighbouring lanes
-            m = 0.f;
+        float m = whole;
+        if (QUANT == SSM_QUANT_BLOCK) {   // 128 columns: 128 / N neighbouring lanes
 #pragma unroll
-            for (int i = 0; i < N; ++i) m = top(m, fabsf(a[i]));
+            for (int i = 0; i < N; ++i) m = top(m, fabsf(y[k][i]));
 #pragma unroll
             for (int o = 64 / N; o > 0; o >>= 1) m = top(m, __shfl_xor_sync(0xffffffffu, m, o));
             if (live && v < nv && v % (128 / N) == 0)
@@ -204,10 +206,10 @@ __global__ void __launch_bounds__(BLOCK) k_rmsnorm_fwd(const FwdArgs p) {
         const float c = code_scale(m);
         if (live && v < nv) {
             unsigned char *dst = p.y8 + row * p.sy8 + (long long)v * N;
-            const uint32_t lo = e4m3x2(a[0] * c, a[1] * c) | (uint32_t)e4m3x2(a[2] * c, a[3] * c) << 16;
+            const uint32_t lo = e4m3x2(y[k][0] * c, y[k][1] * c) | (uint32_t)e4m3x2(y[k][2] * c, y[k][3] * c) << 16;
             if constexpr (N == 8) {
                 const uint32_t hi =
-                    e4m3x2(a[4] * c, a[5] * c) | (uint32_t)e4m3x2(a[6] * c, a[7] * c) << 16;
+                    e4m3x2(y[k][4] * c, y[k][5] * c) | (uint32_t)e4m3x2(y[k][6] * c, y[k][7] * c) << 16;
                 *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, hi);
             } else {
                 *reinterpret_cast<uint32_t *>(dst) = lo;
@@ -287,10 +289,11 @@ struct BwdArgs {
 
 // A team of T threads walks rows with the grid's stride; dweight's partial sums stay in
 // its registers, are added over the block's teams in team order, and leave once.
-template <bool BF16, int V, int T, int BLOCK>
-__global__ void __launch_bounds__(BLOCK) k_rmsnorm_bwd(const BwdArgs p) {
+constexpr int BWD_BLOCK = 512;
+template <bool BF16, int V, int T>
+__global__ void __launch_bounds__(BWD_BLOCK) k_rmsnorm_bwd(const BwdArgs p) {
     using I = Io<BF16>;
-    constexpr int N = I::N, ES = 16 / N, TEAMS = BLOCK / T;
+    constexpr int BLOCK = BWD_BLOCK, N = I::N, ES = 16 / N, TEAMS = BLOCK / T;
     __shared__ float buf[BLOCK / 32];
     __shared__ float add[TEAMS > 1 ? T * N : 1];
     const int lane = threadIdx.x % T, team = threadIdx.x / T;
@@ -300,6 +303,13 @@ __global__ void __launch_bounds__(BLOCK) k_rmsnorm_bwd(const BwdArgs p) {
     for (int k = 0; k < V; ++k)
 #pragma unroll
         for (int i = 0; i < N; ++i) dw[k][i] = 0.f;
+    auto weight = [&](int v, float *w) {
+#pragma unroll
+        for (int q = 0; q < N / 4; ++q)
+            *reinterpret_cast<float4 *>(w + 4 * q) =
+                p.w && v < nv ? __ldg(reinterpret_cast<const float4 *>(p.w) + (long long)v * (N / 4) + q)
+                              : make_float4(1.f, 1.f, 1.f, 1.f);
+    };
     const long long step = (long long)gridDim.x * TEAMS;
     const long long rounds = (p.rows + step - 1) / step;
     for (long long it = 0; it < rounds; ++it) {
@@ -325,15 +335,15 @@ __global__ void __launch_bounds__(BLOCK) k_rmsnorm_bwd(const BwdArgs p) {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int v = lane + k * T;
-            float g[N], r[N];
+            float g[N], r[N], w[N];
             I::unpack(g4[k], g);
             I::unpack(r4[k], r);
+            weight(v, w);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const float xh = r[i] * rstd;
                 dw[k][i] = fmaf(g[i], xh, dw[k][i]);
-                const float w = (p.w && v < nv) ? __ldg(p.w + (long long)v * N + i) : 1.f;
-                dot = fmaf(w * g[i], xh, dot);
+                dot = fmaf(w[i] * g[i], xh, dot);
             }
         }
         dot = team_reduce<T, false>(dot, buf) / (float)p.dim;
@@ -341,15 +351,13 @@ __global__ void __launch_bounds__(BLOCK) k_rmsnorm_bwd(const BwdArgs p) {
         for (int k = 0; k < V; ++k) {
             const int v = lane + k * T;
             if (!live || v >= nv) continue;
-            float g[N], r[N], d[N];
+            float g[N], r[N], d[N], w[N];
             I::unpack(g4[k], g);
             I::unpack(r4[k], r);
             I::unpack(d4[k], d);
+            weight(v, w);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float w = p.w ? __ldg(p.w + (long long)v * N + i) : 1.f;
-                g[i] = fmaf(rstd, w * g[i] - r[i] * rstd * dot, d[i]);
-            }
+            for (int i = 0; i < N; ++i) g[i] = fmaf(rstd, w[i] * g[i] - r[i] * rstd * dot, d[i]);
             *const_cast<uint4 *>(at(p.dx, p.sdx, v)) = I::pack(g);
         }
     }
@@ -426,60 +434,94 @@ __global__ void __launch_bounds__(256) k_rmsnorm_dw(const float *part, float *dw
 
 bool al16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
-// 16-byte pieces of a row, as (pieces a thread, threads a row); 0: the other kernels
+// Pieces a thread and threads a row for rows of nv 16-byte pieces; v 0: the kernels for any
+// row.  Forward: a warp a row while eight pieces a lane suffice, wider teams above; a block a row where
+// there are too few rows for that to fill the card (four warps an SM).
 struct Shape {
     int v, t;
 };
-Shape team_of(int nv) {
+Shape fwd_team(int nv, long long rows) {
+    if (rows < 148 * 4 && nv > 32) {
+        if (nv <= 256) return {1, 256};
+        if (nv <= 512) return {2, 256};
+        if (nv <= 1024) return {4, 256};
+    }
     if (nv <= 32) return {1, 32};
-    if (nv <= 128) return {1, 128};
-    if (nv <= 256) return {1, 256};
-    if (nv <= 512) return {2, 256};
+    if (nv <= 64) return {2, 32};
+    if (nv <= 128) return {4, 32};
+    if (nv <= 256) return {8, 32};
+    if (nv <= 512) return {8, 64};
+    if (nv <= 1024) return {8, 128};
+    if (nv <= 2048) return {8, 256};
+    return {0, 0};
+}
+// Backward: three tensors and the sums of dweight are in registers, so half of that.
+Shape bwd_team(int nv) {
+    if (nv <= 32) return {1, 32};
+    if (nv <= 64) return {2, 32};
+    if (nv <= 128) return {4, 32};
+    if (nv <= 192) return {3, 64};
+    if (nv <= 256) return {4, 64};
+    if (nv <= 512) return {4, 128};
     if (nv <= 1024) return {4, 256};
     if (nv <= 2048) return {4, 512};
     return {0, 0};
 }
 
-constexpr int DW_BLOCKS = 296;   // partial sums of dweight: two blocks an SM
+constexpr int DW_BLOCKS = 148;   // partial sums of dweight: a block an SM
 
 int bwd_blocks(const ssm_rmsnorm_desc_t &d) {
     const int n = d.dtype_io == SSM_BF16 ? 8 : 4;
-    const Shape s = team_of((int)((d.dim + n - 1) / n));
-    const long long teams = s.v ? 512 / s.t : 1;   // rows a block takes at once
+    const Shape s = bwd_team((int)((d.dim + n - 1) / n));
+    const long long teams = s.v ? BWD_BLOCK / s.t : 1;   // rows a block takes at once
     const long long b = (d.rows + teams - 1) / teams;
     return (int)(b < DW_BLOCKS ? b : DW_BLOCKS);
 }
 
-template <bool BF16>
+template <bool BF16, int QUANT>
 cudaError_t fwd(const FwdArgs &a, bool vec, cudaStream_t st) {
     constexpr int N = Io<BF16>::N;
-    const Shape s = vec ? team_of(a.dim / N) : Shape{0, 0};
-    auto go = [&](auto kern, int block, int t) {
+    const Shape s = vec ? fwd_team(a.dim / N, a.rows) : Shape{0, 0};
+    auto go = [&](auto kern, int t) {
+        const int block = t < 256 ? 256 : t;
         const long long per = block / t, grid = (a.rows + per - 1) / per;
         kern<<<(unsigned)grid, block, 0, st>>>(a);
     };
-    if (s.v == 1 && s.t == 32) go(k_rmsnorm_fwd<BF16, 1, 32, 256>, 256, 32);
-    else if (s.v == 1 && s.t == 128) go(k_rmsnorm_fwd<BF16, 1, 128, 256>, 256, 128);
-    else if (s.v == 1) go(k_rmsnorm_fwd<BF16, 1, 256, 256>, 256, 256);
-    else if (s.v == 2) go(k_rmsnorm_fwd<BF16, 2, 256, 256>, 256, 256);
-    else if (s.v == 4 && s.t == 256) go(k_rmsnorm_fwd<BF16, 4, 256, 256>, 256, 256);
-    else if (s.v == 4) go(k_rmsnorm_fwd<BF16, 4, 512, 512>, 512, 512);
+    if (s.t == 32 && s.v == 1) go(k_rmsnorm_fwd<BF16, 1, 32, QUANT>, 32);
+    else if (s.t == 32 && s.v == 2) go(k_rmsnorm_fwd<BF16, 2, 32, QUANT>, 32);
+    else if (s.t == 32 && s.v == 4) go(k_rmsnorm_fwd<BF16, 4, 32, QUANT>, 32);
+    else if (s.t == 32) go(k_rmsnorm_fwd<BF16, 8, 32, QUANT>, 32);
+    else if (s.t == 64) go(k_rmsnorm_fwd<BF16, 8, 64, QUANT>, 64);
+    else if (s.t == 128) go(k_rmsnorm_fwd<BF16, 8, 128, QUANT>, 128);
+    else if (s.t == 256 && s.v == 1) go(k_rmsnorm_fwd<BF16, 1, 256, QUANT>, 256);
+    else if (s.t == 256 && s.v == 2) go(k_rmsnorm_fwd<BF16, 2, 256, QUANT>, 256);
+    else if (s.t == 256 && s.v == 4) go(k_rmsnorm_fwd<BF16, 4, 256, QUANT>, 256);
+    else if (s.t == 256) go(k_rmsnorm_fwd<BF16, 8, 256, QUANT>, 256);
     else k_rmsnorm_fwd_any<BF16><<<(unsigned)a.rows, 256, 0, st>>>(a);
     profile_mark(st, "k_rmsnorm_fwd");
     return cudaGetLastError();
+}
+template <bool BF16>
+cudaError_t fwd(const FwdArgs &a, bool vec, cudaStream_t st) {
+    return a.quant == SSM_QUANT_ROW     ? fwd<BF16, SSM_QUANT_ROW>(a, vec, st)
+           : a.quant == SSM_QUANT_BLOCK ? fwd<BF16, SSM_QUANT_BLOCK>(a, vec, st)
+                                        : fwd<BF16, SSM_QUANT_NONE>(a, vec, st);
 }
 
 template <bool BF16>
 cudaError_t bwd(const BwdArgs &a, bool vec, int blocks, float *dweight, cudaStream_t st) {
     constexpr int N = Io<BF16>::N;
-    const Shape s = vec ? team_of(a.dim / N) : Shape{0, 0};
+    const Shape s = vec ? bwd_team(a.dim / N) : Shape{0, 0};
     cudaError_t e;
-    if (s.v == 1 && s.t == 32) k_rmsnorm_bwd<BF16, 1, 32, 512><<<blocks, 512, 0, st>>>(a);
-    else if (s.v == 1 && s.t == 128) k_rmsnorm_bwd<BF16, 1, 128, 512><<<blocks, 512, 0, st>>>(a);
-    else if (s.v == 1) k_rmsnorm_bwd<BF16, 1, 256, 512><<<blocks, 512, 0, st>>>(a);
-    else if (s.v == 2) k_rmsnorm_bwd<BF16, 2, 256, 512><<<blocks, 512, 0, st>>>(a);
-    else if (s.v == 4 && s.t == 256) k_rmsnorm_bwd<BF16, 4, 256, 512><<<blocks, 512, 0, st>>>(a);
-    else if (s.v == 4) k_rmsnorm_bwd<BF16, 4, 512, 512><<<blocks, 512, 0, st>>>(a);
+    auto go = [&](auto kern) { kern<<<blocks, BWD_BLOCK, 0, st>>>(a); };
+    if (s.t == 32 && s.v == 1) go(k_rmsnorm_bwd<BF16, 1, 32>);
+    else if (s.t == 32 && s.v == 2) go(k_rmsnorm_bwd<BF16, 2, 32>);
+    else if (s.t == 32) go(k_rmsnorm_bwd<BF16, 4, 32>);
+    else if (s.t == 64 && s.v == 3) go(k_rmsnorm_bwd<BF16, 3, 64>);
+    else if (s.t == 64) go(k_rmsnorm_bwd<BF16, 4, 64>);
+    else if (s.t == 128) go(k_rmsnorm_bwd<BF16, 4, 128>);
+    else if (s.t == 256) go(k_rmsnorm_bwd<BF16, 4, 256>);
+    else if (s.t == 512) go(k_rmsnorm_bwd<BF16, 4, 512>);
     else {
         if (a.part) {
             k_rmsnorm_dw_any<BF16><<<dim3((a.dim + 255) / 256, blocks), 256, 0, st>>>(a);
