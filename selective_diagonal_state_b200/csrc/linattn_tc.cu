@@ -96,8 +96,6 @@ __device__ __forceinline__ void tma_prefetch_4d(const void *tmap, int c0, int c1
                  "r"(c0), "r"(c1), "r"(c2), "r"(c3)
                  : "memory");
 }
-// every committed bulk store has reached memory
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
 // One lane of a converged warp, known to the compiler to be one.
 __device__ __forceinline__ bool elect_one() {
     uint32_t one;
@@ -278,6 +276,34 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
     float *f32 = reinterpret_cast<float *>(sm + SM_F32);
     Bars *B = reinterpret_cast<Bars *>(sm + SM_BAR);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // chunk number c of the walk: its first token and its tokens
+    auto chunk = [&](int c) { return C * (first + (REV ? nch - 1 - c : c)); };
+    auto ntok = [&](int t0) { return min(C, len - t0); };
+    const int nboxa = (w.da + 63) / 64, ha = h / w.rep_a, hk = h / w.rep_k, hv = h / w.rep_v;
+    auto load_k = [&](int c) {
+        unsigned char *st = sm + (c & 1) * STAGE + ST_K;
+        mbar_expect_tx(&B->k_full[c & 1], 2 * TILE);
+        tma_load_4d(st, &maps.k, &B->k_full[c & 1], 0, hk, chunk(c), b);
+        // a second box past the head is zeros: state rows that are not there
+        tma_load_4d(st + TILE, &maps.k, &B->k_full[c & 1], 64, hk, chunk(c), b);
+    };
+    auto load_a = [&](int c) {
+        mbar_expect_tx(&B->a_full[c & 1], TILE * nboxa);
+        for (int i = 0; i < nboxa; ++i)
+            tma_load_4d(sm + (c & 1) * STAGE + ST_A + i * TILE, &maps.a, &B->a_full[c & 1], 64 * i, ha, chunk(c), b);
+    };
+    auto load_v = [&](int c) {
+        mbar_expect_tx(&B->v_full[c & 1], TILE);
+        tma_load_4d(sm + (c & 1) * STAGE + ST_V, &maps.v, &B->v_full[c & 1], c0, hv, chunk(c), b);
+    };
+    // the first chunk is on its way before anything else (this thread has set up the barriers)
+    if (tid == 0 && nch > 0) {
+        load_k(0);
+        if (!STATE) {
+            load_a(0);
+            load_v(0);
+        }
+    }
     {   // powers of lam from its logarithm in 64 bits: every one right to half a step
         double g = (double)p.log_decay[h];
         if (g < -1e6) g = -1e6;   // -inf: lam^0 stays 1
@@ -295,19 +321,13 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
     const uint32_t tm = B->tslot;
     const uint32_t lane_q = (uint32_t)(32 * (warp & 3)) << 16;
     const int row = 32 * (warp & 3) + lane;      // token, or state row, of the thread
-    // chunk number c of the walk: its first token and its tokens
-    auto chunk = [&](int c) { return C * (first + (REV ? nch - 1 - c : c)); };
-    auto ntok = [&](int t0) { return min(C, len - t0); };
 
     if (warp == 0) {
         if (lane == 0) {
-            const int nboxa = (w.da + 63) / 64, ha = h / w.rep_a, hk = h / w.rep_k, hv = h / w.rep_v;
-            uint32_t got_a = 0, got_k = 0, got_v = 0;   // loads issued
+            uint32_t got_a = nch > 0, got_k = nch > 0, got_v = nch > 0;   // loads issued
 #pragma unroll 1
             for (int c = 0; c < nch; ++c) {
-                const int s = c & 1, t0 = chunk(c);
                 const uint32_t n = (uint32_t)(c >> 1) - 1u;
-                unsigned char *st = sm + s * STAGE;
                 if (c + 2 < nch) {   // what comes into these slots next, on its way into L2
                     const int tn = chunk(c + 2);
                     tma_prefetch_4d(&maps.k, 0, hk, tn, b);
@@ -316,26 +336,19 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                         for (int i = 0; i < nboxa; ++i) tma_prefetch_4d(&maps.a, 64 * i, ha, tn, b);
                     tma_prefetch_4d(&maps.v, c0, hv, tn, b);
                 }
-                if (c >= 2 && !await(B, &B->k_free[s], n)) break;
-                mbar_expect_tx(&B->k_full[s], 2 * TILE);
-                tma_load_4d(st + ST_K, &maps.k, &B->k_full[s], 0, hk, t0, b);
-                // a second box past the head is zeros: state rows that are not there
-                tma_load_4d(st + ST_K + TILE, &maps.k, &B->k_full[s], 64, hk, t0, b);
+                if (c == 0) continue;
+                if (c >= 2 && !await(B, &B->k_free[c & 1], n)) break;
+                load_k(c);
                 ++got_k;
-                if (!STATE) {
-                    if (c >= 2 && !await(B, &B->a_free[s], n)) break;
-                    mbar_expect_tx(&B->a_full[s], TILE * nboxa);
-                    for (int i = 0; i < nboxa; ++i)
-                        tma_load_4d(st + ST_A + i * TILE, &maps.a, &B->a_full[s], 64 * i, ha, t0, b);
-                    ++got_a;
-                }
-                if (!STATE) {
-                    if (c >= 2 && !await(B, &B->v_free[s], n)) break;
-                    mbar_expect_tx(&B->v_full[s], TILE);
-                    tma_load_4d(st + ST_V, &maps.v, &B->v_full[s], c0, hv, t0, b);
-                    ++got_v;
-                }
+                if (STATE) continue;
+                if (c >= 2 && !await(B, &B->a_free[c & 1], n)) break;
+                load_a(c);
+                ++got_a;
+                if (c >= 2 && !await(B, &B->v_free[c & 1], n)) break;
+                load_v(c);
+                ++got_v;
             }
+            if (STATE) got_a = got_v = 0;
             // no copy is in flight when the block ends
 #pragma unroll 1
             for (uint32_t i = 0; i < 6; ++i) {
@@ -439,7 +452,6 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                 bulk_wait_read_all();
                 mbar_arrive(OUT == 1 ? &B->a_free[c & 1] : &B->v_free[c & 1]);
             }
-            bulk_wait_all();
         }
         __syncwarp();
     } else if (!STATE && warp >= 4 && warp < 12) {
@@ -619,21 +631,17 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
         float *dst = seg ? (STATE ? slot : nullptr) : w.s_out ? w.s_out + outside : nullptr;
         const int stc = seg ? 1 : w.st_c, cols = row < w.da ? w.dc - c0 : 0;
         const long long at = (long long)row * (seg ? w.dc : w.st_a) + (long long)c0 * stc;
-        // eight columns at a time through the last eight registers, the others moving down: rolled
-        // loops, so that what runs once does not crowd out the code of the chunks
-        auto turn = [&]() {
-#pragma unroll
-            for (int j = 0; j < 28; ++j) S[j] = S[j + 4];
-        };
+        // 32 columns at a time (the latency of memory twice)
         const int got = src ? cols : 0;
 #pragma unroll 1
-        for (int j = 0; j < 64; j += 8) {
-            turn();
+        for (int j = 0; j < 64; j += 32) {
             const float *q = src + at + j * stc;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                S[28 + i].x = j + 2 * i < got ? q[2 * i * stc] : 0.f;
-                S[28 + i].y = j + 2 * i + 1 < got ? q[(2 * i + 1) * stc] : 0.f;
+            for (int i = 0; i < 16; ++i) S[i] = S[i + 16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                S[16 + i].x = j + 2 * i < got ? q[2 * i * stc] : 0.f;
+                S[16 + i].y = j + 2 * i + 1 < got ? q[(2 * i + 1) * stc] : 0.f;
             }
         }
 #pragma unroll 1
@@ -678,7 +686,8 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                     if (j + 2 * i < cols) q[2 * i * stc] = S[i].x;
                     if (j + 2 * i + 1 < cols) q[(2 * i + 1) * stc] = S[i].y;
                 }
-                turn();
+#pragma unroll
+                for (int i = 0; i < 28; ++i) S[i] = S[i + 4];   // rolled: what runs once stays small
             }
         }
     }
@@ -727,7 +736,7 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
 }
 
 // The state entering every segment, in place of what the segment adds, and the state that
-// leaves the walk: a thread an element, the segments in the walk's order.
+// leaves the walk: a thread an element, the segments in the walk's order, eight loads at a time.
 __global__ void __launch_bounds__(256) k_la_segments(const __grid_constant__ Args A) {
     const LaArgs &p = A.p;
     const LaWalk &w = p.w[blockIdx.y];
@@ -738,14 +747,25 @@ __global__ void __launch_bounds__(256) k_la_segments(const __grid_constant__ Arg
     double g = (double)p.log_decay[h];
     if (g < -1e6) g = -1e6;
     const long long at = (long long)bh * w.da * w.dc, ext = at + (long long)a * w.st_a + (long long)c * w.st_c;
+    const long long step = (long long)BH * w.da * w.dc;
+    float *slot = A.seg[blockIdx.y] + at + e;
     float E = w.s_in ? w.s_in[ext] : 0.f;
-    for (int i = 0; i < A.nseg; ++i) {
-        const int s = w.rev ? A.nseg - 1 - i : i;
-        const int n = min(max(len - s * A.G * C, 0), A.G * C);   // its tokens
-        float *q = A.seg[blockIdx.y] + (long long)s * BH * w.da * w.dc + at + e;
-        const float add = *q;
-        *q = E;
-        E = fmaf((float)exp(g * n), E, add);
+    const float whole = (float)exp(g * (A.G * C));   // the decay of a whole segment
+    for (int i0 = 0; i0 < A.nseg; i0 += 8) {
+        float add[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int s = w.rev ? A.nseg - 1 - i0 - k : i0 + k;
+            add[k] = i0 + k < A.nseg ? slot[s * step] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (i0 + k >= A.nseg) break;
+            const int s = w.rev ? A.nseg - 1 - i0 - k : i0 + k;
+            const int n = min(max(len - s * A.G * C, 0), A.G * C);   // its tokens
+            slot[s * step] = E;
+            E = fmaf(n == A.G * C ? whole : (float)exp(g * n), E, add[k]);
+        }
     }
     if (w.s_out) w.s_out[ext] = E;
 }
@@ -784,15 +804,16 @@ cudaError_t set_smem() {
 bool la_chunked_sizes(int bf16, int da, int dc) { return bf16 && da <= 128 && da % 8 == 0 && dc % 8 == 0; }
 
 // Segments of the sequences (of `L` tokens; `items` blocks without segments): the count with
-// the shortest estimate, where a chunk's walk takes 1 and its state alone 1/2, 148 blocks run
-// at a time, and the two more launches take 4.
+// the shortest estimate, in chunks of a walk (about 2.5 us): a block takes 3 to begin and end,
+// a chunk whose state alone is walked 0.7, the pass over the segments' states and its launch
+// 3, and 148 blocks run at a time.
 int la_segments(long long L, long long items) {
     const long long nc = (L + la::C - 1) / la::C;
     double best = 0;
     int pick = 1;
     for (long long n = 1; n <= nc && n <= 64; ++n) {
         const long long g = (nc + n - 1) / n, seg = (nc + g - 1) / g, waves = (items * seg + 147) / 148;
-        const double t = (double)(waves * g) * (seg > 1 ? 1.5 : 1.0) + (seg > 1 ? 4 : 0);
+        const double t = waves * (g + 3.0) + (seg > 1 ? waves * (0.7 * g + 3.0) + 3.0 : 0.0);
         if (seg == n && (n == 1 || t < 0.95 * best)) {
             best = t;
             pick = (int)n;
