@@ -215,47 +215,33 @@ struct Bars {
     uint64_t o_tile;                            // the output in shared memory, or stored
     uint64_t end;
     uint32_t tslot;
-    int abort;
+    int failed;
 };
 static_assert(sizeof(Bars) <= 224, "barrier space");
 
-// Bounded wait for the completion number `n` (from 0) of a barrier; false, with the error word
-// and the block's abort flag raised, when it does not come or another role has given up.  The
-// hint lets the hardware keep the thread suspended: polls of 16 waiting warps would take the
-// issue slots that the others need.
+// Bounded wait for the completion number `n` (from 0) of a barrier; false when it does not
+// come, and every role that waits for one that has given up gives up too, the block's error
+// raised at its end.  The hint lets the hardware keep the thread suspended between polls.
 constexpr uint32_t POLL_NS = 20000, POLLS = 1u << 15;   // about half a second
-__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(POLL_NS)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool await(Bars *B, uint64_t *bar, uint32_t n) {
+__device__ __forceinline__ bool await(uint64_t *bar, uint32_t n) {
     const uint32_t a = smem_u32(bar);
 #pragma unroll 1
     for (uint32_t i = 0; i < POLLS; ++i) {
-        if (poll(a, n & 1u)) return true;
-        if (*reinterpret_cast<volatile int *>(&B->abort)) return false;
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(a), "r"(n & 1u), "r"(POLL_NS)
+            : "memory");
+        if (ok) return true;
     }
-    *reinterpret_cast<volatile int *>(&B->abort) = 1;
-    atomicCAS(&ssm_la_error_word, 0, 1);
     return false;
 }
-// A wait for what is in flight when the block ends, whatever the others do.
-__device__ __forceinline__ void drain(uint64_t *bar, uint32_t n) {
-    const uint32_t a = smem_u32(bar);
-#pragma unroll 1
-    for (uint32_t i = 0; i < POLLS && !poll(a, n & 1u); ++i) {
-    }
-}
 // The same for a whole warp, all lanes alike.
-__device__ __forceinline__ bool await_warp(Bars *B, uint64_t *bar, uint32_t n) {
-    return __all_sync(0xffffffffu, await(B, bar, n));
+__device__ __forceinline__ bool await_warp(uint64_t *bar, uint32_t n) {
+    return __all_sync(0xffffffffu, await(bar, n));
 }
 // One arrival a warp, after all its lanes are done.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
@@ -319,14 +305,19 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
     __syncthreads();
     fence_after_sync();
     const uint32_t tm = B->tslot;
+    // a role that leaves its loop early says so
+    auto over = [&](bool all) {
+        if (!all) B->failed = 1;
+    };
     const uint32_t lane_q = (uint32_t)(32 * (warp & 3)) << 16;
     const int row = 32 * (warp & 3) + lane;      // token, or state row, of the thread
 
     if (warp == 0) {
         if (lane == 0) {
             uint32_t got_a = nch > 0, got_k = nch > 0, got_v = nch > 0;   // loads issued
+            int c = 0;
 #pragma unroll 1
-            for (int c = 0; c < nch; ++c) {
+            for (; c < nch; ++c) {
                 const uint32_t n = (uint32_t)(c >> 1) - 1u;
                 if (c + 2 < nch) {   // what comes into these slots next, on its way into L2
                     const int tn = chunk(c + 2);
@@ -337,24 +328,25 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                     tma_prefetch_4d(&maps.v, c0, hv, tn, b);
                 }
                 if (c == 0) continue;
-                if (c >= 2 && !await(B, &B->k_free[c & 1], n)) break;
+                if (c >= 2 && !await(&B->k_free[c & 1], n)) break;
                 load_k(c);
                 ++got_k;
                 if (STATE) continue;
-                if (c >= 2 && !await(B, &B->a_free[c & 1], n)) break;
+                if (c >= 2 && !await(&B->a_free[c & 1], n)) break;
                 load_a(c);
                 ++got_a;
-                if (c >= 2 && !await(B, &B->v_free[c & 1], n)) break;
+                if (c >= 2 && !await(&B->v_free[c & 1], n)) break;
                 load_v(c);
                 ++got_v;
             }
+            over(c >= nch);
             if (STATE) got_a = got_v = 0;
             // no copy is in flight when the block ends
 #pragma unroll 1
             for (uint32_t i = 0; i < 6; ++i) {
                 const uint32_t got = i < 2 ? got_a : i < 4 ? got_k : got_v, back = 1 + (i & 1);
                 uint64_t *full = i < 2 ? B->a_full : i < 4 ? B->k_full : B->v_full;
-                if (got >= back) drain(&full[(got - back) & 1], (got - back) >> 1);
+                if (got >= back) await(&full[(got - back) & 1], (got - back) >> 1);
             }
         }
         __syncwarp();
@@ -382,26 +374,27 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             auto mnmaj = [](uint32_t u, int s) { return desc<TILE>(u + STEP * s); };
             auto scores = [&](int c) {
                 const uint32_t st = u0 + ((c & 1) ? STAGE >> 4 : 0u);
-                if (!await(B, &B->k_full[c & 1], (uint32_t)c >> 1) || !await(B, &B->a_full[c & 1], (uint32_t)c >> 1)) return false;
-                if (c > 0 && !await(B, &B->sc_read, (uint32_t)c - 1u)) return false;
+                if (!await(&B->k_full[c & 1], (uint32_t)c >> 1) || !await(&B->a_full[c & 1], (uint32_t)c >> 1)) return false;
+                if (c > 0 && !await(&B->sc_read, (uint32_t)c - 1u)) return false;
                 fence_after_sync();
                 over_head(tm + TM_SC, st + (ST_A >> 4), st + (ST_K >> 4), id_sc, kmaj);
                 mma_commit(&B->sc);
                 return true;
             };
+            int c = STATE ? 0 : -1;
 #pragma unroll 1
-            for (int c = STATE ? 0 : -1; c < nch; ++c) {
+            for (; c < nch; ++c) {
                 const uint32_t st = u0 + ((c & 1) ? STAGE >> 4 : 0u);
                 if (c >= 0) {
-                    if (STATE && !await(B, &B->k_full[c & 1], (uint32_t)c >> 1)) break;
-                    if (c > 0 && !await(B, &B->kv_read, (uint32_t)c - 1u)) break;
-                    if (!await(B, &B->vp[0], (uint32_t)c)) break;
+                    if (STATE && !await(&B->k_full[c & 1], (uint32_t)c >> 1)) break;
+                    if (c > 0 && !await(&B->kv_read, (uint32_t)c - 1u)) break;
+                    if (!await(&B->vp[0], (uint32_t)c)) break;
                     fence_after_sync();
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
                         mma_bf16(tm + TM_KV, mnmaj(st + (ST_K >> 4), s), mnmaj(u0 + (SM_VP >> 4), s), id_kv, s > 0);
                     mma_commit(&B->kv[0]);
-                    if (!await(B, &B->vp[1], (uint32_t)c)) break;
+                    if (!await(&B->vp[1], (uint32_t)c)) break;
                     fence_after_sync();
 #pragma unroll
                     for (int s = 4; s < 8; ++s)
@@ -409,8 +402,8 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                     mma_commit(&B->kv[1]);
                     mma_commit(&B->k_free[c & 1]);
                     if (!STATE) {
-                        if (!await(B, &B->s, (uint32_t)c)) break;
-                        if (c > 0 && !await(B, &B->o_read, (uint32_t)c - 1u)) break;
+                        if (!await(&B->s, (uint32_t)c)) break;
+                        if (c > 0 && !await(&B->o_read, (uint32_t)c - 1u)) break;
                         fence_after_sync();
                         over_head(tm + TM_OS, st + (ST_A >> 4), u0 + (SM_S >> 4), id_n, mnmaj);
                         mma_commit(&B->as);
@@ -420,7 +413,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                 if (!STATE) {
                     if (c + 1 < nch && !scores(c + 1)) break;
                     if (c >= 0) {
-                        if (!await(B, &B->v_full[c & 1], (uint32_t)c >> 1) || !await(B, &B->p, (uint32_t)c)) break;
+                        if (!await(&B->v_full[c & 1], (uint32_t)c >> 1) || !await(&B->p, (uint32_t)c)) break;
                         fence_after_sync();
 #pragma unroll
                         for (int s = 0; s < 8; ++s)
@@ -430,16 +423,18 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                     }
                 }
             }
+            over(c >= nch);
             mma_commit(&B->end);   // every MMA is over before tensor memory goes
-            drain(&B->end, 0u);
+            await(&B->end, 0u);
         }
         __syncwarp();
     } else if (!STATE && warp == 2) {
         if (lane == 0) {
+            int c = 0;
 #pragma unroll 1
-            for (int c = 0; c < nch; ++c) {
+            for (; c < nch; ++c) {
                 const int t0 = chunk(c), n = ntok(t0);
-                if (!await(B, &B->o_tile, (uint32_t)c)) break;
+                if (!await(&B->o_tile, (uint32_t)c)) break;
                 // what is past L or the head is not written
                 if (OUT == 1) {   // (rows behind the sequence hold nothing that is read)
                     const unsigned char *at = sm + (c & 1) * STAGE + ST_A;
@@ -452,16 +447,18 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                 bulk_wait_read_all();
                 mbar_arrive(OUT == 1 ? &B->a_free[c & 1] : &B->v_free[c & 1]);
             }
+            over(c >= nch);
         }
         __syncwarp();
     } else if (!STATE && warp >= 4 && warp < 12) {
         const int half = (warp - 4) >> 2, qd = warp & 3;
         const long long ob = b * w.so[0] + h * w.so[2] + c0 + 32 * half;
         const int nq = min(4, (w.dc - c0 - 32 * half) / 8);   // 8-column pieces of the output (<= 0: none)
+        int c = 0;
 #pragma unroll 1
-        for (int c = 0; c < nch; ++c) {
+        for (; c < nch; ++c) {
             const int t0 = chunk(c), n = ntok(t0);
-            if (!await_warp(B, &B->sc, (uint32_t)c)) break;
+            if (!await_warp(&B->sc, (uint32_t)c)) break;
             fence_after_sync();
             // P[i][j] = read write lam^{|i - j|} (a_i . k_j) on one side of the diagonal, 32 columns
             // at a time
@@ -515,7 +512,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             tmem_wait_st();
             fence_before_sync();
             warp_arrive(&B->p);
-            if (!await_warp(B, &B->o, (uint32_t)c)) break;
+            if (!await_warp(&B->o, (uint32_t)c)) break;
             fence_after_sync();
             const float e = w.read * f32[F_PW + max(0, REV ? n - 1 - row : row + 1)];
             const float2 ee = make_float2(e, e);
@@ -556,6 +553,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             fence_proxy_async();
             warp_arrive(&B->o_tile);
         }
+        over(c >= nch);
     } else if (warp >= 16) {
         // V' = write lam^.. v, from memory by way of registers half a chunk ahead: it does not wait
         // for a free V tile, nor hold one.  A thread takes 8 columns of four rows of each half.
@@ -563,29 +561,30 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
         const float2 minus = make_float2(-1.f, -1.f);
         const __nv_bfloat16 *vg = reinterpret_cast<const __nv_bfloat16 *>(w.v) + b * w.sv[0] + (h / w.rep_v) * w.sv[2] + c0 + col;
         const bool mine = c0 + col < w.dc;
-        uint4 cur[4], nxt[4];
+        uint4 cur[4], nxt[4] = {};
         auto fetch = [&](int hh) {   // rows of half hh & 1 of chunk hh >> 1
             const int t0 = chunk(hh >> 1), n = ntok(t0), r0 = (t >> 3) + 64 * (hh & 1);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 nxt[i] = mine && r0 + 16 * i < n ? ld_once(vg + (long long)(t0 + r0 + 16 * i) * w.sv[1]) : make_uint4(0u, 0u, 0u, 0u);
         };
-        if (nch > 0) fetch(0);
+        int hh = -1;
 #pragma unroll 1
-        for (int hh = 0; hh < 2 * nch; ++hh) {
+        for (; hh < 2 * nch; ++hh) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
+            if (hh + 1 < 2 * nch) fetch(hh + 1);
+            if (hh < 0) continue;
             const int c = hh >> 1, z = hh & 1;
             unsigned char *st = sm + (c & 1) * STAGE;
             const int t0 = chunk(c), n = ntok(t0);
             const bool fix = n < C && t0 + n < p.L;   // rows of other tokens (TMA fills those past L with zeros)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
-            if (hh + 1 < 2 * nch) fetch(hh + 1);
             if (fix) {   // the scores have read K
-                if (!await_warp(B, &B->k_full[c & 1], (uint32_t)c >> 1)) break;
-                if (!STATE && !await_warp(B, &B->v_full[c & 1], (uint32_t)c >> 1)) break;
-                if (!STATE && !await_warp(B, &B->sc, (uint32_t)c)) break;
+                if (!await_warp(&B->k_full[c & 1], (uint32_t)c >> 1)) break;
+                if (!STATE && !await_warp(&B->v_full[c & 1], (uint32_t)c >> 1)) break;
+                if (!STATE && !await_warp(&B->sc, (uint32_t)c)) break;
             }
-            if (c > 0 && !await_warp(B, &B->kv[z], (uint32_t)c - 1u)) break;   // this half has been read
+            if (c > 0 && !await_warp(&B->kv[z], (uint32_t)c - 1u)) break;   // this half has been read
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
                 const int r = (t >> 3) + 64 * z + 16 * i;
@@ -620,6 +619,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             fence_proxy_async();
             warp_arrive(&B->vp[z]);
         }
+        over(hh >= 2 * nch);
     } else if (warp >= 12) {
         float2 S[32];
         const bool seg = A.nseg > 1;
@@ -644,10 +644,11 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                 S[16 + i].y = j + 2 * i + 1 < got ? q[(2 * i + 1) * stc] : 0.f;
             }
         }
+        int c = 0;
 #pragma unroll 1
-        for (int c = 0; c < nch; ++c) {
+        for (; c < nch; ++c) {
             if (!STATE) {   // S in bf16, the layout of a V tile; A S of the chunk before has read it
-                if (c > 0 && !await_warp(B, &B->as, (uint32_t)c - 1u)) break;
+                if (c > 0 && !await_warp(&B->as, (uint32_t)c - 1u)) break;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     const uint4 v = make_uint4(pack2(S[4 * q].x, S[4 * q].y), pack2(S[4 * q + 1].x, S[4 * q + 1].y),
@@ -660,7 +661,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             const float E = f32[F_PW + ntok(chunk(c))];
             const float2 EE = make_float2(E, E);
             const uint32_t tk = tm + TM_KV + lane_q;
-            if (!await_warp(B, &B->kv[1], (uint32_t)c)) break;
+            if (!await_warp(&B->kv[1], (uint32_t)c)) break;
             fence_after_sync();
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -677,6 +678,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             fence_before_sync();
             warp_arrive(&B->kv_read);
         }
+        over(c >= nch);
         if (dst) {
 #pragma unroll 1
             for (int j = 0; j < 64; j += 8) {
@@ -719,7 +721,7 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
         // an arrival a warp
         for (uint64_t *q : {&B->vp[0], &B->vp[1], &B->s, &B->kv_read}) mbar_init(q, 4);
         for (uint64_t *q : {&B->p, &B->sc_read, &B->o_read, &B->o_tile}) mbar_init(q, 8);
-        B->abort = 0;
+        B->failed = 0;
         mbar_fence_init();
     }
     if (threadIdx.x / 32 == 1) tmem_alloc(&B->tslot, TM_COLS);
@@ -729,6 +731,7 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
         w.rev ? walk<STATE, true, 1>(A, maps, w, wi, slice, bh, sg, sm) : walk<STATE, false, 1>(A, maps, w, wi, slice, bh, sg, sm);
     fence_before_sync();
     __syncthreads();
+    if (threadIdx.x == 0 && B->failed) atomicCAS(&ssm_la_error_word, 0, 1);
     if (threadIdx.x / 32 == 1) {
         fence_after_sync();
         tmem_dealloc(B->tslot, TM_COLS);
