@@ -631,17 +631,48 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
         float *dst = seg ? (STATE ? slot : nullptr) : w.s_out ? w.s_out + outside : nullptr;
         const int stc = seg ? 1 : w.st_c, cols = row < w.da ? w.dc - c0 : 0;
         const long long at = (long long)row * (seg ? w.dc : w.st_a) + (long long)c0 * stc;
-        // 32 columns at a time (the latency of memory twice)
-        const int got = src ? cols : 0;
+        // 32 columns at a time.  Where a row of the state lies along its columns, a warp's 32 rows pass
+        // through the operand's place, so that memory is read and written in whole lines (a thread
+        // with a row of its own took 5 us for a head of 128 x 128); transposed, the lanes are
+        // neighbours already.
+        float *tile = reinterpret_cast<float *>(sm + SM_S) + 32 * 32 * (warp & 3);
+        auto place = [&](int r, int q) { return tile + 32 * r + ((q ^ (r & 7)) << 2); };   // 4 columns q of row r
+        const long long rows0 = (long long)(row - lane) * (seg ? w.dc : w.st_a) + c0 + lane;
+        const int dense_rows = w.da - (row - lane);   // of the warp's rows, those of the state
 #pragma unroll 1
         for (int j = 0; j < 64; j += 32) {
-            const float *q = src + at + j * stc;
 #pragma unroll
             for (int i = 0; i < 16; ++i) S[i] = S[i + 16];
+            if (!src) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                S[16 + i].x = j + 2 * i < got ? q[2 * i * stc] : 0.f;
-                S[16 + i].y = j + 2 * i + 1 < got ? q[(2 * i + 1) * stc] : 0.f;
+                for (int i = 16; i < 32; ++i) S[i] = make_float2(0.f, 0.f);
+            } else if (stc == 1) {
+                const float *q = src + rows0 + j;
+                const bool mine = c0 + j + lane < w.dc;
+#pragma unroll 1
+                for (int r0 = 0; r0 < 32; r0 += 16) {
+                    float x[16];
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        x[r] = mine && r0 + r < dense_rows ? q[(long long)(r0 + r) * (seg ? w.dc : w.st_a)] : 0.f;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) place(r0 + r, lane >> 2)[lane & 3] = x[r];
+                }
+                __syncwarp();
+#pragma unroll
+                for (int q4 = 0; q4 < 8; ++q4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(place(lane, q4));
+                    S[16 + 2 * q4] = make_float2(v.x, v.y);
+                    S[17 + 2 * q4] = make_float2(v.z, v.w);
+                }
+                __syncwarp();
+            } else {
+                const float *q = src + at + j * stc;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    S[16 + i].x = j + 2 * i < cols ? q[2 * i * stc] : 0.f;
+                    S[16 + i].y = j + 2 * i + 1 < cols ? q[(2 * i + 1) * stc] : 0.f;
+                }
             }
         }
         int c = 0;
@@ -680,16 +711,31 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
         }
         over(c >= nch);
         if (dst) {
+            if (!STATE && c >= nch && nch > 0) await_warp(&B->as, (uint32_t)nch - 1u);   // A S has read the operand
 #pragma unroll 1
-            for (int j = 0; j < 64; j += 8) {
-                float *q = dst + at + j * stc;
+            for (int j = 0; j < 64; j += 32) {
+                if (stc == 1) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (j + 2 * i < cols) q[2 * i * stc] = S[i].x;
-                    if (j + 2 * i + 1 < cols) q[(2 * i + 1) * stc] = S[i].y;
+                    for (int q4 = 0; q4 < 8; ++q4)
+                        *reinterpret_cast<float4 *>(place(lane, q4)) =
+                            make_float4(S[2 * q4].x, S[2 * q4].y, S[2 * q4 + 1].x, S[2 * q4 + 1].y);
+                    __syncwarp();
+                    float *q = dst + rows0 + j;
+                    if (c0 + j + lane < w.dc)
+#pragma unroll 4
+                        for (int r = 0; r < min(32, dense_rows); ++r)
+                            q[(long long)r * (seg ? w.dc : w.st_a)] = place(r, lane >> 2)[lane & 3];
+                    __syncwarp();
+                } else {
+                    float *q = dst + at + j * stc;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (j + 2 * i < cols) q[2 * i * stc] = S[i].x;
+                        if (j + 2 * i + 1 < cols) q[(2 * i + 1) * stc] = S[i].y;
+                    }
                 }
 #pragma unroll
-                for (int i = 0; i < 28; ++i) S[i] = S[i + 4];   // rolled: what runs once stays small
+                for (int i = 0; i < 16; ++i) S[i] = S[i + 16];
             }
         }
     }
