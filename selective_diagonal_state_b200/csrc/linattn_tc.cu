@@ -14,15 +14,16 @@
 // that is itself stored as bf16.
 //
 // A block walks one segment of one (batch row, head), 64 columns of v and the state: per
-// chunk 80 KB come in by TMA and 16 KB go out.  One block an SM, its 20 warps with a role each:
+// chunk 80 KB come in by TMA and 16 KB go out.  One block an SM, its 28 warps with a role each:
 //     warp 0       TMA loads, two chunks ahead, each tile again as soon as its last reader is done
-//     warp 1       all MMAs, per chunk: K^T V', A S, the next chunk's A K^T, P V
+//     warps 1, 3   MMAs: K^T V'; and A S, P V, then the next chunk's A K^T (one warp for all of them
+//                  spent half of a chunk's time in its waits between the products)
 //     warp 2       TMA stores of the output, which is laid over the chunk's V tile (fp32: A tiles)
 //     warps 4-11   P from the scores, and the output (a thread a token and half of the columns)
-//     warps 12-15  the state (a thread a state row, 64 values in registers)
-//     warps 16-19  V', in halves of 64 tokens, v straight from L2
-// so that P is made while K^T V' and A S run, and V', the state and the output of one chunk
-// beside the products of the next.  Every role runs its own code once a chunk, so the walk is
+//     warps 12-19  the state (a thread a state row and half of the columns, in registers)
+//     warps 20-27  V', in halves of 64 tokens, v straight from L2
+// so that P, V', the state and the output of one chunk are made
+// beside the products of others.  Every role runs its own code once a chunk, so the walk is
 // compiled for each direction and kind of output and its loops stay rolled: instruction fetch
 // was what bound a kernel of the same structure with unrolled, run-time variants (185 KB of
 // code, 613 us for 4 x 16384 tokens of 16 heads; 72 KB, 412 us).
@@ -42,7 +43,7 @@ using namespace umma;
 using chunkc::WAIT_LIMIT;
 
 constexpr int C = 128;                   // tokens of a chunk
-constexpr int THREADS = 640;
+constexpr int THREADS = 896;
 constexpr uint32_t TILE = 16384;         // 128 rows x 128 bytes (64 bf16), 128-byte swizzle
 constexpr uint32_t ST_A = 0, ST_K = 2 * TILE, ST_V = 4 * TILE, STAGE = 5 * TILE;
 constexpr uint32_t SM_VP = 2 * STAGE;    // V' in three parts
@@ -81,12 +82,16 @@ template <uint32_t LBO> __device__ __forceinline__ uint64_t desc(uint32_t units)
     constexpr uint32_t hi = (1024u >> 4) | 1u << 14 | LAYOUT_SW128 << 29;
     return (uint64_t)hi << 32 | (units | (LBO >> 4) << 16);
 }
-// 16 bytes that stay out of L1
-__device__ __forceinline__ uint4 ld_once(const void *p) {
+// 16 bytes that stay out of L1, or zeros; one statement, so that nothing waits for the load but
+// the values' use (behind a branch, the choice of the value does).
+__device__ __forceinline__ uint4 ld_once(const void *p, bool on) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}\n"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((uint32_t)on));
     return v;
 }
 // Prefetch of a tile into L2.
@@ -211,9 +216,10 @@ struct Bars {
     uint64_t a_free[2], k_free[2], v_free[2];   // tiles read by their last product
     uint64_t sc, kv[2], as, o;                  // products done: scores; K^T V' (halves of the tokens); A S; P V
     uint64_t p, vp[2], s;                       // operands written: P, V' (halves), S
-    uint64_t sc_read, kv_read, o_read;          // results fetched from tensor memory
+    uint64_t kv_read, o_read;                   // results fetched from tensor memory
     uint64_t o_tile;                            // the output in shared memory, or stored
-    uint64_t end;
+    uint64_t fixed;                             // rows of other tokens are zeros (one chunk of a walk at most)
+    uint64_t end[2];
     uint32_t tslot;
     int failed;
 };
@@ -265,6 +271,9 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
     // chunk number c of the walk: its first token and its tokens
     auto chunk = [&](int c) { return C * (first + (REV ? nch - 1 - c : c)); };
     auto ntok = [&](int t0) { return min(C, len - t0); };
+    // the chunk, if any, whose tiles hold rows of other tokens (TMA fills those past L with zeros)
+    const int shared = nch > 0 && (first + nch) * C > len && len < p.L ? (REV ? 0 : nch - 1) : -1;
+    auto dirty = [&](int c) { return c == shared; };
     const int nboxa = (w.da + 63) / 64, ha = h / w.rep_a, hk = h / w.rep_k, hv = h / w.rep_v;
     auto load_k = [&](int c) {
         unsigned char *st = sm + (c & 1) * STAGE + ST_K;
@@ -350,43 +359,22 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 || (!STATE && warp == 3)) {
         if (elect_one()) {
-            const uint32_t base = smem_u32(sm);
             constexpr uint32_t id_sc = idesc_bf16(128, 128, false, false), id_n = idesc_bf16(128, 64, false, true);
             constexpr uint32_t id_kv = idesc_bf16(128, 192, true, true);
             // descriptors: their address field counts 16-byte units; along a row, 16 values are 2 of them
-            const uint32_t u0 = base >> 4;
+            const uint32_t u0 = smem_u32(sm) >> 4;
             const int ks = (w.da + 15) / 16;
             constexpr uint32_t HALF = TILE >> 4, STEP = 2048 >> 4;   // the next 64 values of the rows; the next 16 rows
-            // a chunk's products over the head dimension, for whole heads of 128 without a loop: the
-            // thread that issues is on the critical path, and a rolled loop takes it 130 cycles an MMA
-            auto over_head = [&](uint32_t d, uint32_t a, uint32_t bb, uint32_t id, auto desc_b) {
-                if (ks == 8) {
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) mma_bf16(d, desc<16u>(a + (s >> 2) * HALF + (s & 3) * 2u), desc_b(bb, s), id, s > 0);
-                } else {
-#pragma unroll 1
-                    for (int s = 0; s < ks; ++s) mma_bf16(d, desc<16u>(a + (s >> 2) * HALF + (s & 3) * 2u), desc_b(bb, s), id, s > 0);
-                }
-            };
             auto kmaj = [](uint32_t u, int s) { return desc<16u>(u + (s >> 2) * HALF + (s & 3) * 2u); };
             auto mnmaj = [](uint32_t u, int s) { return desc<TILE>(u + STEP * s); };
-            auto scores = [&](int c) {
-                const uint32_t st = u0 + ((c & 1) ? STAGE >> 4 : 0u);
-                if (!await(&B->k_full[c & 1], (uint32_t)c >> 1) || !await(&B->a_full[c & 1], (uint32_t)c >> 1)) return false;
-                if (c > 0 && !await(&B->sc_read, (uint32_t)c - 1u)) return false;
-                fence_after_sync();
-                over_head(tm + TM_SC, st + (ST_A >> 4), st + (ST_K >> 4), id_sc, kmaj);
-                mma_commit(&B->sc);
-                return true;
-            };
-            int c = STATE ? 0 : -1;
+            int c = 0;
+            if (warp == 1) {   // K^T V', the smallest part of V' in the last columns
 #pragma unroll 1
-            for (; c < nch; ++c) {
-                const uint32_t st = u0 + ((c & 1) ? STAGE >> 4 : 0u);
-                if (c >= 0) {
-                    if (STATE && !await(&B->k_full[c & 1], (uint32_t)c >> 1)) break;
+                for (; c < nch; ++c) {
+                    const uint32_t st = u0 + ((c & 1) ? STAGE >> 4 : 0u);
+                    if (!await(&B->k_full[c & 1], (uint32_t)c >> 1)) break;
                     if (c > 0 && !await(&B->kv_read, (uint32_t)c - 1u)) break;
                     if (!await(&B->vp[0], (uint32_t)c)) break;
                     fence_after_sync();
@@ -401,19 +389,31 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                         mma_bf16(tm + TM_KV, mnmaj(st + (ST_K >> 4), s), mnmaj(u0 + (SM_VP >> 4), s), id_kv, true);
                     mma_commit(&B->kv[1]);
                     mma_commit(&B->k_free[c & 1]);
-                    if (!STATE) {
+                }
+            } else {
+                // a chunk's products over the head dimension, for whole heads of 128 without a loop: the
+                // thread that issues is on the critical path, and a rolled loop takes it 130 cycles an MMA
+                auto over_head = [&](uint32_t d, uint32_t a, uint32_t bb, uint32_t id, auto desc_b) {
+                    if (ks == 8) {
+#pragma unroll
+                        for (int s = 0; s < 8; ++s) mma_bf16(d, kmaj(a, s), desc_b(bb, s), id, s > 0);
+                    } else {
+#pragma unroll 1
+                        for (int s = 0; s < ks; ++s) mma_bf16(d, kmaj(a, s), desc_b(bb, s), id, s > 0);
+                    }
+                };
+#pragma unroll 1
+                for (c = -1; c < nch; ++c) {
+                    const uint32_t st = u0 + ((c & 1) ? STAGE >> 4 : 0u);
+                    if (c >= 0) {
                         if (!await(&B->s, (uint32_t)c)) break;
                         if (c > 0 && !await(&B->o_read, (uint32_t)c - 1u)) break;
                         fence_after_sync();
                         over_head(tm + TM_OS, st + (ST_A >> 4), u0 + (SM_S >> 4), id_n, mnmaj);
                         mma_commit(&B->as);
                         if (OUT == 0) mma_commit(&B->a_free[c & 1]);   // else warp 2, when the output has left the tile
-                    }
-                }
-                if (!STATE) {
-                    if (c + 1 < nch && !scores(c + 1)) break;
-                    if (c >= 0) {
                         if (!await(&B->v_full[c & 1], (uint32_t)c >> 1) || !await(&B->p, (uint32_t)c)) break;
+                        if (dirty(c) && !await(&B->fixed, 0u)) break;
                         fence_after_sync();
 #pragma unroll
                         for (int s = 0; s < 8; ++s)
@@ -421,11 +421,20 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                         mma_commit(&B->o);
                         if (OUT == 1) mma_commit(&B->v_free[c & 1]);
                     }
+                    if (c + 1 < nch) {   // the scores of the next chunk; P's warps have fetched this one's
+                        const uint32_t sn = u0 + ((c & 1) ? 0u : STAGE >> 4), n = (uint32_t)(c + 1) >> 1;
+                        if (!await(&B->k_full[(c + 1) & 1], n) || !await(&B->a_full[(c + 1) & 1], n)) break;
+                        fence_after_sync();
+                        over_head(tm + TM_SC, sn + (ST_A >> 4), sn + (ST_K >> 4), id_sc, kmaj);
+                        mma_commit(&B->sc);
+                        mma_commit(&B->k_free[(c + 1) & 1]);
+                    }
                 }
             }
             over(c >= nch);
-            mma_commit(&B->end);   // every MMA is over before tensor memory goes
-            await(&B->end, 0u);
+            uint64_t *end = &B->end[warp >> 1];
+            mma_commit(end);   // every MMA is over before tensor memory goes
+            await(end, 0u);
         }
         __syncwarp();
     } else if (!STATE && warp == 2) {
@@ -433,14 +442,14 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             int c = 0;
 #pragma unroll 1
             for (; c < nch; ++c) {
-                const int t0 = chunk(c), n = ntok(t0);
+                const int t0 = chunk(c);
                 if (!await(&B->o_tile, (uint32_t)c)) break;
                 // what is past L or the head is not written
                 if (OUT == 1) {   // (rows behind the sequence hold nothing that is read)
                     const unsigned char *at = sm + (c & 1) * STAGE + ST_A;
                     tma_store_4d(&maps.o, at, c0, h, t0, b);
                     if (c0 + 32 < w.dc) tma_store_4d(&maps.o, at + TILE, c0 + 32, h, t0, b);
-                } else if (!(n < C && t0 + n < p.L)) {
+                } else if (!dirty(c)) {
                     tma_store_4d(&maps.o, sm + (c & 1) * STAGE + ST_V, c0, h, t0, b);
                 }
                 bulk_commit();
@@ -470,10 +479,6 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                 uint32_t x[16], y[16];
                 if (!zero) {
                     tmem_get32(tm + TM_SC + lane_q + 32u * jb, x, y);
-                }
-                if (z == 1) {
-                    fence_before_sync();
-                    warp_arrive(&B->sc_read);
                 }
                 if (zero) {
 #pragma unroll
@@ -518,7 +523,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             const float2 ee = make_float2(e, e);
             // 16 columns at a time: over the chunk's V tile (fp32: its A tiles), from where warp 2 stores
             // whole chunks, or, where rows behind the sequence must stay as they are, straight to memory
-            const bool tile = OUT == 0 && !(n < C && t0 + n < p.L);
+            const bool tile = OUT == 0 && !dirty(c);
             unsigned char *vt = sm + (c & 1) * STAGE + ST_V + row * 128;
             unsigned char *at32 = sm + (c & 1) * STAGE + ST_A + half * TILE + row * 128;
             const long long at = ob + (long long)(t0 + row) * w.so[1];
@@ -554,31 +559,39 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             warp_arrive(&B->o_tile);
         }
         over(c >= nch);
-    } else if (warp >= 16) {
-        // V' = write lam^.. v, from memory by way of registers half a chunk ahead: it does not wait
-        // for a free V tile, nor hold one.  A thread takes 8 columns of four rows of each half.
-        const int t = tid - 512, col = 8 * (t & 7);
+    } else if (warp >= 20) {
+        // V' = write lam^.. v, from memory by way of registers a chunk ahead: it does not wait
+        // for a free V tile, nor hold one.  A thread takes 8 columns of two rows of each half.
+        const int t = tid - 640, col = 8 * (t & 7);
         const float2 minus = make_float2(-1.f, -1.f);
         const __nv_bfloat16 *vg = reinterpret_cast<const __nv_bfloat16 *>(w.v) + b * w.sv[0] + (h / w.rep_v) * w.sv[2] + c0 + col;
         const bool mine = c0 + col < w.dc;
-        uint4 cur[4], nxt[4] = {};
-        auto fetch = [&](int hh) {   // rows of half hh & 1 of chunk hh >> 1
-            const int t0 = chunk(hh >> 1), n = ntok(t0), r0 = (t >> 3) + 64 * (hh & 1);
+        // the rows of each half have registers of their own: a move would wait for the load
+        uint4 cur[2], lo[2] = {}, hi[2] = {};
+        auto fetch = [&](uint4 (&x)[2], int c, int z) {
+            const int t0 = chunk(c), r0 = (t >> 3) + 64 * z, n = ntok(t0);
+            const __nv_bfloat16 *q = vg + (long long)(t0 + r0) * w.sv[1];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                nxt[i] = mine && r0 + 16 * i < n ? ld_once(vg + (long long)(t0 + r0 + 16 * i) * w.sv[1]) : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 2; ++i)
+                x[i] = ld_once(q + 32 * i * w.sv[1], mine && r0 + 32 * i < n);
         };
-        int hh = -1;
+        int hh = -2;
 #pragma unroll 1
         for (; hh < 2 * nch; ++hh) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
-            if (hh + 1 < 2 * nch) fetch(hh + 1);
-            if (hh < 0) continue;
             const int c = hh >> 1, z = hh & 1;
+            if (z == 0) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) cur[i] = lo[i];
+                if (c + 1 < nch) fetch(lo, c + 1, 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) cur[i] = hi[i];
+                if (c + 1 < nch) fetch(hi, c + 1, 1);
+            }
+            if (c < 0) continue;
             unsigned char *st = sm + (c & 1) * STAGE;
-            const int t0 = chunk(c), n = ntok(t0);
-            const bool fix = n < C && t0 + n < p.L;   // rows of other tokens (TMA fills those past L with zeros)
+            const int n = ntok(chunk(c));
+            const bool fix = dirty(c);
             if (fix) {   // the scores have read K
                 if (!await_warp(&B->k_full[c & 1], (uint32_t)c >> 1)) break;
                 if (!STATE && !await_warp(&B->v_full[c & 1], (uint32_t)c >> 1)) break;
@@ -586,13 +599,11 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             }
             if (c > 0 && !await_warp(&B->kv[z], (uint32_t)c - 1u)) break;   // this half has been read
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-                const int r = (t >> 3) + 64 * z + 16 * i;
+            for (int i = 0; i < 2; ++i) {
+                const int r = (t >> 3) + 64 * z + 32 * i;
                 const uint32_t off = (uint32_t)r * 128u + (uint32_t)((col / 8) ^ (r & 7)) * 16u;
                 const uint4 x = cur[0];
                 cur[0] = cur[1];
-                cur[1] = cur[2];
-                cur[2] = cur[3];
                 if (fix && r >= n) {
                     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
                     if (!STATE) *reinterpret_cast<uint4 *>(st + ST_V + off) = zero;
@@ -618,10 +629,12 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             }
             fence_proxy_async();
             warp_arrive(&B->vp[z]);
+            if (fix && z == 1) warp_arrive(&B->fixed);
         }
         over(hh >= 2 * nch);
     } else if (warp >= 12) {
-        float2 S[32];
+        float2 S[16];
+        const int half = (warp - 12) >> 2, col = c0 + 32 * half;   // the thread's first column
         const bool seg = A.nseg > 1;
         // where the state comes from and goes to: the caller's, or the segment's slot (a segment
         // that only adds starts from zero; the states that leave are k_la_segments' work)
@@ -629,50 +642,49 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
         const long long outside = (long long)bh * w.da * w.dc;
         const float *src = seg ? (STATE ? nullptr : slot) : w.s_in ? w.s_in + outside : nullptr;
         float *dst = seg ? (STATE ? slot : nullptr) : w.s_out ? w.s_out + outside : nullptr;
-        const int stc = seg ? 1 : w.st_c, cols = row < w.da ? w.dc - c0 : 0;
-        const long long at = (long long)row * (seg ? w.dc : w.st_a) + (long long)c0 * stc;
-        // 32 columns at a time.  Where a row of the state lies along its columns, a warp's 32 rows pass
-        // through the operand's place, so that memory is read and written in whole lines (a thread
-        // with a row of its own took 5 us for a head of 128 x 128); transposed, the lanes are
-        // neighbours already.
-        float *tile = reinterpret_cast<float *>(sm + SM_S) + 32 * 32 * (warp & 3);
-        auto place = [&](int r, int q) { return tile + 32 * r + ((q ^ (r & 7)) << 2); };   // 4 columns q of row r
-        const long long rows0 = (long long)(row - lane) * (seg ? w.dc : w.st_a) + c0 + lane;
-        const int dense_rows = w.da - (row - lane);   // of the warp's rows, those of the state
-#pragma unroll 1
-        for (int j = 0; j < 64; j += 32) {
+        const int stc = seg ? 1 : w.st_c, cols = row < w.da ? w.dc - col : 0;
+        const long long at = (long long)row * (seg ? w.dc : w.st_a) + (long long)col * stc;
+        // Where a row of the state lies along its columns, a warp's 32 rows pass, 16 columns at a time,
+        // through 2 KB of the operand's place, so that memory is read and written in whole sectors
+        // (a thread with a row of its own took 5 us for a head of 128 x 128); transposed, the lanes
+        // are neighbours already.
+        float *tile = reinterpret_cast<float *>(sm + SM_S) + 512 * (warp - 12);
+        auto place = [&](int r, int q) { return tile + 16 * r + ((q ^ ((r >> 1) & 3)) << 2); };   // 4 columns q of row r
+        const int sub = lane >> 4, sc = lane & 15;   // a lane's row of two, and its column
+        const int rs = seg ? w.dc : w.st_a, rows0 = (row - lane + sub) * rs + col + sc;
+        const int dense_rows = w.da - (row - lane) - sub;   // of the lane's rows, those of the state
+        if (!src) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) S[i] = S[i + 16];
-            if (!src) {
+            for (int i = 0; i < 16; ++i) S[i] = make_float2(0.f, 0.f);
+        } else if (stc == 1) {
 #pragma unroll
-                for (int i = 16; i < 32; ++i) S[i] = make_float2(0.f, 0.f);
-            } else if (stc == 1) {
-                const float *q = src + rows0 + j;
-                const bool mine = c0 + j + lane < w.dc;
+            for (int z = 0; z < 2; ++z) {
+                const float *q = src + rows0 + 16 * z;
+                const bool mine = col + 16 * z + sc < w.dc;
 #pragma unroll 1
                 for (int r0 = 0; r0 < 32; r0 += 16) {
-                    float x[16];
+                    float x[8];
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        x[r] = mine && r0 + r < dense_rows ? q[(long long)(r0 + r) * (seg ? w.dc : w.st_a)] : 0.f;
+                    for (int r = 0; r < 8; ++r) x[r] = mine && r0 + 2 * r < dense_rows ? q[(r0 + 2 * r) * rs] : 0.f;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) place(r0 + r, lane >> 2)[lane & 3] = x[r];
+                    for (int r = 0; r < 8; ++r) place(r0 + 2 * r + sub, sc >> 2)[sc & 3] = x[r];
                 }
                 __syncwarp();
 #pragma unroll
-                for (int q4 = 0; q4 < 8; ++q4) {
+                for (int q4 = 0; q4 < 4; ++q4) {
                     const float4 v = *reinterpret_cast<const float4 *>(place(lane, q4));
-                    S[16 + 2 * q4] = make_float2(v.x, v.y);
-                    S[17 + 2 * q4] = make_float2(v.z, v.w);
+                    S[8 * z + 2 * q4] = make_float2(v.x, v.y);
+                    S[8 * z + 2 * q4 + 1] = make_float2(v.z, v.w);
                 }
                 __syncwarp();
-            } else {
-                const float *q = src + at + j * stc;
+            }
+            asm volatile("bar.sync 8, 256;\n" ::: "memory");   // the operand may be written
+        } else {
+            const float *q = src + at;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    S[16 + i].x = j + 2 * i < cols ? q[2 * i * stc] : 0.f;
-                    S[16 + i].y = j + 2 * i + 1 < cols ? q[(2 * i + 1) * stc] : 0.f;
-                }
+            for (int i = 0; i < 16; ++i) {
+                S[i].x = 2 * i < cols ? q[2 * i * stc] : 0.f;
+                S[i].y = 2 * i + 1 < cols ? q[(2 * i + 1) * stc] : 0.f;
             }
         }
         int c = 0;
@@ -681,21 +693,21 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             if (!STATE) {   // S in bf16, the layout of a V tile; A S of the chunk before has read it
                 if (c > 0 && !await_warp(&B->as, (uint32_t)c - 1u)) break;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                for (int q = 0; q < 4; ++q) {
                     const uint4 v = make_uint4(pack2(S[4 * q].x, S[4 * q].y), pack2(S[4 * q + 1].x, S[4 * q + 1].y),
                                                pack2(S[4 * q + 2].x, S[4 * q + 2].y), pack2(S[4 * q + 3].x, S[4 * q + 3].y));
-                    *reinterpret_cast<uint4 *>(sm + SM_S + row * 128 + ((q ^ (row & 7)) << 4)) = v;
+                    *reinterpret_cast<uint4 *>(sm + SM_S + row * 128 + (((q + 4 * half) ^ (row & 7)) << 4)) = v;
                 }
                 fence_proxy_async();
                 warp_arrive(&B->s);
             }
             const float E = f32[F_PW + ntok(chunk(c))];
             const float2 EE = make_float2(E, E);
-            const uint32_t tk = tm + TM_KV + lane_q;
+            const uint32_t tk = tm + TM_KV + lane_q + 32u * half;
             if (!await_warp(&B->kv[1], (uint32_t)c)) break;
             fence_after_sync();
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 4; ++q) {
                 uint32_t x[8], y[8];
                 tmem_get8x2(tk + 64u + 8u * q, tk + 128u + 8u * q, x, y);
                 float2 small[4];
@@ -712,30 +724,27 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
         over(c >= nch);
         if (dst) {
             if (!STATE && c >= nch && nch > 0) await_warp(&B->as, (uint32_t)nch - 1u);   // A S has read the operand
-#pragma unroll 1
-            for (int j = 0; j < 64; j += 32) {
-                if (stc == 1) {
+            if (stc == 1) {
 #pragma unroll
-                    for (int q4 = 0; q4 < 8; ++q4)
+                for (int z = 0; z < 2; ++z) {
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4)
                         *reinterpret_cast<float4 *>(place(lane, q4)) =
-                            make_float4(S[2 * q4].x, S[2 * q4].y, S[2 * q4 + 1].x, S[2 * q4 + 1].y);
+                            make_float4(S[8 * z + 2 * q4].x, S[8 * z + 2 * q4].y, S[8 * z + 2 * q4 + 1].x, S[8 * z + 2 * q4 + 1].y);
                     __syncwarp();
-                    float *q = dst + rows0 + j;
-                    if (c0 + j + lane < w.dc)
-#pragma unroll 4
-                        for (int r = 0; r < min(32, dense_rows); ++r)
-                            q[(long long)r * (seg ? w.dc : w.st_a)] = place(r, lane >> 2)[lane & 3];
+                    float *q = dst + rows0 + 16 * z;
+                    if (col + 16 * z + sc < w.dc)
+#pragma unroll 1
+                        for (int r = 0; r < min(32, dense_rows); r += 2) q[r * rs] = place(r + sub, sc >> 2)[sc & 3];
                     __syncwarp();
-                } else {
-                    float *q = dst + at + j * stc;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (j + 2 * i < cols) q[2 * i * stc] = S[i].x;
-                        if (j + 2 * i + 1 < cols) q[(2 * i + 1) * stc] = S[i].y;
-                    }
                 }
+            } else {
+                float *q = dst + at;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[i] = S[i + 16];
+                for (int i = 0; i < 16; ++i) {
+                    if (2 * i < cols) q[2 * i * stc] = S[i].x;
+                    if (2 * i + 1 < cols) q[(2 * i + 1) * stc] = S[i].y;
+                }
             }
         }
     }
@@ -752,7 +761,7 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
     const int bh = id % BH;
     id /= BH;
     const int sg = id % A.nseg, wi = id / A.nseg;
-    const LaWalk &w = A.p.w[wi];
+    const LaWalk w = A.p.w[wi];   // by value: with the index unknown, every use would load from memory
     const Maps &maps = wi == 0 ? m0 : wi == 1 ? m1 : m2;
     if (64 * slice >= w.dc) return;
     extern __shared__ unsigned char smem_raw[];
@@ -762,11 +771,10 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i)
             for (uint64_t *q : {&B->a_full[i], &B->k_full[i], &B->v_full[i], &B->a_free[i], &B->k_free[i], &B->v_free[i]})
-                mbar_init(q, 1);
-        for (uint64_t *q : {&B->sc, &B->kv[0], &B->kv[1], &B->as, &B->o, &B->end}) mbar_init(q, 1);
+                mbar_init(q, q == &B->k_free[i] && !STATE ? 2 : 1);   // K has two readers
+        for (uint64_t *q : {&B->sc, &B->kv[0], &B->kv[1], &B->as, &B->o, &B->end[0], &B->end[1]}) mbar_init(q, 1);
         // an arrival a warp
-        for (uint64_t *q : {&B->vp[0], &B->vp[1], &B->s, &B->kv_read}) mbar_init(q, 4);
-        for (uint64_t *q : {&B->p, &B->sc_read, &B->o_read, &B->o_tile}) mbar_init(q, 8);
+        for (uint64_t *q : {&B->vp[0], &B->vp[1], &B->s, &B->kv_read, &B->fixed, &B->p, &B->o_read, &B->o_tile}) mbar_init(q, 8);
         B->failed = 0;
         mbar_fence_init();
     }
