@@ -270,9 +270,12 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // chunk number c of the walk: its first token and its tokens
     auto chunk = [&](int c) { return C * (first + (REV ? nch - 1 - c : c)); };
-    auto ntok = [&](int t0) { return min(C, len - t0); };
+    // the chunk that the sequence ends in, if it is a short one, and its tokens
+    const bool ends = nch > 0 && (first + nch) * C > len;
+    const int ragged = ends ? (REV ? 0 : nch - 1) : -1, rest = len - C * (first + nch - 1);
+    auto ntok = [&](int c) { return c == ragged ? rest : C; };
     // the chunk, if any, whose tiles hold rows of other tokens (TMA fills those past L with zeros)
-    const int shared = nch > 0 && (first + nch) * C > len && len < p.L ? (REV ? 0 : nch - 1) : -1;
+    const int shared = len < p.L ? ragged : -1;
     auto dirty = [&](int c) { return c == shared; };
     const int nboxa = (w.da + 63) / 64, ha = h / w.rep_a, hk = h / w.rep_k, hv = h / w.rep_v;
     auto load_k = [&](int c) {
@@ -466,7 +469,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
         int c = 0;
 #pragma unroll 1
         for (; c < nch; ++c) {
-            const int t0 = chunk(c), n = ntok(t0);
+            const int t0 = chunk(c), n = ntok(c);
             if (!await_warp(&B->sc, (uint32_t)c)) break;
             fence_after_sync();
             // P[i][j] = read write lam^{|i - j|} (a_i . k_j) on one side of the diagonal, 32 columns
@@ -564,33 +567,31 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
         // for a free V tile, nor hold one.  A thread takes 8 columns of two rows of each half.
         const int t = tid - 640, col = 8 * (t & 7);
         const float2 minus = make_float2(-1.f, -1.f);
-        const __nv_bfloat16 *vg = reinterpret_cast<const __nv_bfloat16 *>(w.v) + b * w.sv[0] + (h / w.rep_v) * w.sv[2] + c0 + col;
-        const bool mine = c0 + col < w.dc;
         // the rows of each half have registers of their own: a move would wait for the load
+        const bool mine = c0 + col < w.dc;
+        const long long by = 64 * w.sv[1];   // bytes from a row to the 32nd after it
+        const char *vg = reinterpret_cast<const char *>(reinterpret_cast<const __nv_bfloat16 *>(w.v) + b * w.sv[0] + hv * w.sv[2] +
+                                                        c0 + col + (long long)(chunk(0) + (t >> 3)) * w.sv[1]);
         uint4 cur[2], lo[2] = {}, hi[2] = {};
-        auto fetch = [&](uint4 (&x)[2], int c, int z) {
-            const int t0 = chunk(c), r0 = (t >> 3) + 64 * z, n = ntok(t0);
-            const __nv_bfloat16 *q = vg + (long long)(t0 + r0) * w.sv[1];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                x[i] = ld_once(q + 32 * i * w.sv[1], mine && r0 + 32 * i < n);
-        };
         int hh = -2;
 #pragma unroll 1
         for (; hh < 2 * nch; ++hh) {
-            const int c = hh >> 1, z = hh & 1;
+            const int c = hh >> 1, z = hh & 1, live = c + 1 < nch && mine ? ntok(c + 1) - (t >> 3) : 0;   // rows of the next chunk
             if (z == 0) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) cur[i] = lo[i];
-                if (c + 1 < nch) fetch(lo, c + 1, 0);
+                cur[0] = lo[0];
+                cur[1] = lo[1];
+                lo[0] = ld_once(vg, live > 0);
+                lo[1] = ld_once(vg + by, live > 32);
             } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) cur[i] = hi[i];
-                if (c + 1 < nch) fetch(hi, c + 1, 1);
+                cur[0] = hi[0];
+                cur[1] = hi[1];
+                hi[0] = ld_once(vg + 2 * by, live > 64);
+                hi[1] = ld_once(vg + 3 * by, live > 96);
+                vg += REV ? -4 * by : 4 * by;
             }
             if (c < 0) continue;
             unsigned char *st = sm + (c & 1) * STAGE;
-            const int n = ntok(chunk(c));
+            const int n = ntok(c);
             const bool fix = dirty(c);
             if (fix) {   // the scores have read K
                 if (!await_warp(&B->k_full[c & 1], (uint32_t)c >> 1)) break;
@@ -701,7 +702,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                 fence_proxy_async();
                 warp_arrive(&B->s);
             }
-            const float E = f32[F_PW + ntok(chunk(c))];
+            const float E = f32[F_PW + ntok(c)];
             const float2 EE = make_float2(E, E);
             const uint32_t tk = tm + TM_KV + lane_q + 32u * half;
             if (!await_warp(&B->kv[1], (uint32_t)c)) break;
