@@ -294,14 +294,6 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
         mbar_expect_tx(&B->v_full[c & 1], TILE);
         tma_load_4d(sm + (c & 1) * STAGE + ST_V, &maps.v, &B->v_full[c & 1], c0, hv, chunk(c), b);
     };
-    // the first chunk is on its way before anything else (this thread has set up the barriers)
-    if (tid == 0 && nch > 0) {
-        load_k(0);
-        if (!STATE) {
-            load_a(0);
-            load_v(0);
-        }
-    }
     {   // powers of lam from its logarithm in 64 bits: every one right to half a step
         double g = (double)p.log_decay[h];
         if (g < -1e6) g = -1e6;   // -inf: lam^0 stays 1
@@ -326,20 +318,20 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
 
     if (warp == 0) {
         if (lane == 0) {
-            uint32_t got_a = nch > 0, got_k = nch > 0, got_v = nch > 0;   // loads issued
+            uint32_t got_a = 0, got_k = 0, got_v = 0;   // loads issued
             int c = 0;
 #pragma unroll 1
             for (; c < nch; ++c) {
                 const uint32_t n = (uint32_t)(c >> 1) - 1u;
                 if (c + 2 < nch) {   // what comes into these slots next, on its way into L2
                     const int tn = chunk(c + 2);
-                    tma_prefetch_4d(&maps.k, 0, hk, tn, b);
-                    if (w.da > 64) tma_prefetch_4d(&maps.k, 64, hk, tn, b);
-                    if (!STATE)
-                        for (int i = 0; i < nboxa; ++i) tma_prefetch_4d(&maps.a, 64 * i, ha, tn, b);
+#pragma unroll 1
+                    for (int i = 0; i < nboxa; ++i) {
+                        tma_prefetch_4d(&maps.k, 64 * i, hk, tn, b);
+                        if (!STATE) tma_prefetch_4d(&maps.a, 64 * i, ha, tn, b);
+                    }
                     tma_prefetch_4d(&maps.v, c0, hv, tn, b);
                 }
-                if (c == 0) continue;
                 if (c >= 2 && !await(&B->k_free[c & 1], n)) break;
                 load_k(c);
                 ++got_k;
@@ -352,7 +344,6 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                 ++got_v;
             }
             over(c >= nch);
-            if (STATE) got_a = got_v = 0;
             // no copy is in flight when the block ends
 #pragma unroll 1
             for (uint32_t i = 0; i < 6; ++i) {
@@ -368,9 +359,8 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             constexpr uint32_t id_kv = idesc_bf16(128, 192, true, true);
             // descriptors: their address field counts 16-byte units; along a row, 16 values are 2 of them
             const uint32_t u0 = smem_u32(sm) >> 4;
-            const int ks = (w.da + 15) / 16;
             constexpr uint32_t HALF = TILE >> 4, STEP = 2048 >> 4;   // the next 64 values of the rows; the next 16 rows
-            auto kmaj = [](uint32_t u, int s) { return desc<16u>(u + (s >> 2) * HALF + (s & 3) * 2u); };
+            auto kmaj = [](uint32_t u, int s) { return desc<16u>(u + s * 2u); };
             auto mnmaj = [](uint32_t u, int s) { return desc<TILE>(u + STEP * s); };
             int c = 0;
             if (warp == 1) {   // K^T V', the smallest part of V' in the last columns
@@ -379,31 +369,30 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                     const uint32_t st = u0 + ((c & 1) ? STAGE >> 4 : 0u);
                     if (!await(&B->k_full[c & 1], (uint32_t)c >> 1)) break;
                     if (c > 0 && !await(&B->kv_read, (uint32_t)c - 1u)) break;
-                    if (!await(&B->vp[0], (uint32_t)c)) break;
-                    fence_after_sync();
+                    int z = 0;
+#pragma unroll 1
+                    for (; z < 2; ++z) {
+                        if (!await(&B->vp[z], (uint32_t)c)) break;
+                        fence_after_sync();
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        mma_bf16(tm + TM_KV, mnmaj(st + (ST_K >> 4), s), mnmaj(u0 + (SM_VP >> 4), s), id_kv, s > 0);
-                    mma_commit(&B->kv[0]);
-                    if (!await(&B->vp[1], (uint32_t)c)) break;
-                    fence_after_sync();
-#pragma unroll
-                    for (int s = 4; s < 8; ++s)
-                        mma_bf16(tm + TM_KV, mnmaj(st + (ST_K >> 4), s), mnmaj(u0 + (SM_VP >> 4), s), id_kv, true);
-                    mma_commit(&B->kv[1]);
+                        for (int s = 0; s < 4; ++s)
+                            mma_bf16(tm + TM_KV, mnmaj(st + (ST_K >> 4) + 4 * STEP * z, s), mnmaj(u0 + (SM_VP >> 4) + 4 * STEP * z, s),
+                                     id_kv, s > 0 || z > 0);
+                        mma_commit(&B->kv[z]);
+                    }
+                    if (z < 2) break;
                     mma_commit(&B->k_free[c & 1]);
                 }
             } else {
-                // a chunk's products over the head dimension, for whole heads of 128 without a loop: the
-                // thread that issues is on the critical path, and a rolled loop takes it 130 cycles an MMA
-                auto over_head = [&](uint32_t d, uint32_t a, uint32_t bb, uint32_t id, auto desc_b) {
-                    if (ks == 8) {
-#pragma unroll
-                        for (int s = 0; s < 8; ++s) mma_bf16(d, kmaj(a, s), desc_b(bb, s), id, s > 0);
-                    } else {
+                // a chunk's product over the head dimension, 64 values at a time (heads padded with the
+                // tiles' zeros): rolled to one MMA the loop took 130 cycles an MMA, and all of them
+                // in a row are more code than the fetch keeps up with
+                auto over_head = [&](uint32_t d, uint32_t a, uint32_t bb, uint32_t id, bool kb) {
 #pragma unroll 1
-                        for (int s = 0; s < ks; ++s) mma_bf16(d, kmaj(a, s), desc_b(bb, s), id, s > 0);
-                    }
+                    for (int q = 0; q < nboxa; ++q)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            mma_bf16(d, kmaj(a + HALF * q, s), kb ? kmaj(bb + HALF * q, s) : mnmaj(bb + 4 * STEP * q, s), id, s > 0 || q > 0);
                 };
 #pragma unroll 1
                 for (c = -1; c < nch; ++c) {
@@ -412,15 +401,17 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                         if (!await(&B->s, (uint32_t)c)) break;
                         if (c > 0 && !await(&B->o_read, (uint32_t)c - 1u)) break;
                         fence_after_sync();
-                        over_head(tm + TM_OS, st + (ST_A >> 4), u0 + (SM_S >> 4), id_n, mnmaj);
+                        over_head(tm + TM_OS, st + (ST_A >> 4), u0 + (SM_S >> 4), id_n, false);
                         mma_commit(&B->as);
                         if (OUT == 0) mma_commit(&B->a_free[c & 1]);   // else warp 2, when the output has left the tile
                         if (!await(&B->v_full[c & 1], (uint32_t)c >> 1) || !await(&B->p, (uint32_t)c)) break;
                         if (dirty(c) && !await(&B->fixed, 0u)) break;
                         fence_after_sync();
+#pragma unroll 1
+                        for (int q = 0; q < 2; ++q)
 #pragma unroll
-                        for (int s = 0; s < 8; ++s)
-                            mma_bf16_ts(tm + TM_OI, tm + TM_P + 8u * s, mnmaj(st + (ST_V >> 4), s), id_n, s > 0);
+                            for (int s = 0; s < 4; ++s)
+                                mma_bf16_ts(tm + TM_OI, tm + TM_P + 32u * q + 8u * s, mnmaj(st + (ST_V >> 4) + 4 * STEP * q, s), id_n, s > 0 || q > 0);
                         mma_commit(&B->o);
                         if (OUT == 1) mma_commit(&B->v_free[c & 1]);
                     }
@@ -428,7 +419,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                         const uint32_t sn = u0 + ((c & 1) ? 0u : STAGE >> 4), n = (uint32_t)(c + 1) >> 1;
                         if (!await(&B->k_full[(c + 1) & 1], n) || !await(&B->a_full[(c + 1) & 1], n)) break;
                         fence_after_sync();
-                        over_head(tm + TM_SC, sn + (ST_A >> 4), sn + (ST_K >> 4), id_sc, kmaj);
+                        over_head(tm + TM_SC, sn + (ST_A >> 4), sn + (ST_K >> 4), id_sc, true);
                         mma_commit(&B->sc);
                         mma_commit(&B->k_free[(c + 1) & 1]);
                     }
@@ -511,7 +502,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                     }
                 }
                 const int left = n - 32 * jb;   // columns of this sequence
-                if (left < 32) {   // tokens past it do not count, whatever they hold
+                if (__builtin_expect(left < 32, 0)) {   // tokens past it do not count, whatever they hold
 #pragma unroll
                     for (int u = 0; u < 16; ++u) o[u] = 2 * u + 1 < left ? o[u] : 2 * u < left ? o[u] & 0xffffu : 0u;
                 }
@@ -546,7 +537,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                 }
                 const uint4 r0 = make_uint4(pack2(o[0].x, o[0].y), pack2(o[1].x, o[1].y), pack2(o[2].x, o[2].y), pack2(o[3].x, o[3].y));
                 const uint4 r1 = make_uint4(pack2(o[4].x, o[4].y), pack2(o[5].x, o[5].y), pack2(o[6].x, o[6].y), pack2(o[7].x, o[7].y));
-                if (tile) {
+                if (__builtin_expect(tile, 1)) {
                     const int q = 4 * half + 2 * z;
                     *reinterpret_cast<uint4 *>(vt + ((q ^ (row & 7)) << 4)) = r0;
                     *reinterpret_cast<uint4 *>(vt + (((q + 1) ^ (row & 7)) << 4)) = r1;
@@ -593,7 +584,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             unsigned char *st = sm + (c & 1) * STAGE;
             const int n = ntok(c);
             const bool fix = dirty(c);
-            if (fix) {   // the scores have read K
+            if (__builtin_expect(fix, 0)) {   // the scores have read K
                 if (!await_warp(&B->k_full[c & 1], (uint32_t)c >> 1)) break;
                 if (!STATE && !await_warp(&B->v_full[c & 1], (uint32_t)c >> 1)) break;
                 if (!STATE && !await_warp(&B->sc, (uint32_t)c)) break;
@@ -605,7 +596,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                 const uint32_t off = (uint32_t)r * 128u + (uint32_t)((col / 8) ^ (r & 7)) * 16u;
                 const uint4 x = cur[0];
                 cur[0] = cur[1];
-                if (fix && r >= n) {
+                if (__builtin_expect(fix && r >= n, 0)) {
                     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
                     if (!STATE) *reinterpret_cast<uint4 *>(st + ST_V + off) = zero;
                     *reinterpret_cast<uint4 *>(st + ST_K + off) = zero;
@@ -630,7 +621,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             }
             fence_proxy_async();
             warp_arrive(&B->vp[z]);
-            if (fix && z == 1) warp_arrive(&B->fixed);
+            if (__builtin_expect(fix && z == 1, 0)) warp_arrive(&B->fixed);
         }
         over(hh >= 2 * nch);
     } else if (warp >= 12) {
