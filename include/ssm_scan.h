@@ -545,8 +545,8 @@ typedef struct ssm_linattn_desc {
 } ssm_linattn_desc_t;
 
 /* SSM_LINATTN_AUTO: the tensor-core walk over 128-token chunks where it applies (bf16,
- * head dims that are multiples of 8 and at most 128, 16-byte aligned tensors and strides),
- * else the token-by-token recurrence; SSM_LINATTN_RECURRENT: always the latter.  Results
+ * head dims that are multiples of 8 and at most 128, 16-byte aligned tensors and strides,
+ * and more than 1024 / head dim tokens), else the token-by-token recurrence; SSM_LINATTN_RECURRENT: always the latter.  Results
  * are equal up to rounding. */
 enum ssm_linattn_route { SSM_LINATTN_AUTO = 0, SSM_LINATTN_RECURRENT = 1 };
 

@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(256) k_la_recurrent(const LaArgs p, int slices
     constexpr int DA = 8 * NR;
     __shared__ __align__(16) float sa[TT][DA], sk[TT][DA];
     __shared__ float sv[TT][32], part[TT][8][32];
-    const LaWalk &w = p.w[blockIdx.y];
+    const LaWalk w = p.w[blockIdx.y];
     const int bh = blockIdx.x / slices, c0 = 32 * (blockIdx.x - bh * slices);
     if (c0 >= w.dc) return;
     const int b = bh / p.H, h = bh - b * p.H;
@@ -51,30 +51,40 @@ __global__ void __launch_bounds__(256) k_la_recurrent(const LaArgs p, int slices
     const long long bk = b * w.sk[0] + (h / w.rep_k) * w.sk[2];
     const long long bv = b * w.sv[0] + (h / w.rep_v) * w.sv[2];
     const long long bo = b * w.so[0] + h * w.so[2];
+    // the next tile's values wait in registers while this one is walked
+    constexpr int NA = TT * DA / 256, NV = TT * 32 / 256;
+    float xa[NA], xk[NA], xv[NV];
+    auto fetch = [&](int i0) {
+        const int m = min(TT, n - i0);
+#pragma unroll
+        for (int u = 0; u < NA; ++u) {
+            const int e = tid + 256 * u, i = e / DA, a = e - i * DA;
+            const long long t = w.rev ? n - 1 - i0 - i : i0 + i;
+            const bool on = i < m && a < w.da;
+            xa[u] = on && w.o ? ld_io(w.a, ba + t * w.sa[1] + a, p.bf16) : 0.f;
+            xk[u] = on ? ld_io(w.k, bk + t * w.sk[1] + a, p.bf16) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            const int e = tid + 256 * u, i = e >> 5, c = c0 + (e & 31);
+            const long long t = w.rev ? n - 1 - i0 - i : i0 + i;
+            xv[u] = i < m && c < w.dc ? ld_io(w.v, bv + t * w.sv[1] + c, p.bf16) * w.write : 0.f;
+        }
+    };
+    if (n > 0) fetch(0);
     for (int i0 = 0; i0 < n; i0 += TT) {
         const int m = min(TT, n - i0);
         __syncthreads();
-        for (int e = tid; e < TT * DA; e += 256) {
-            const int i = e / DA, a = e - i * DA;
-            float x = 0.f, y = 0.f;
-            if (i < m && a < w.da) {
-                const long long t = w.rev ? n - 1 - i0 - i : i0 + i;
-                if (w.o) x = ld_io(w.a, ba + t * w.sa[1] + a, p.bf16);
-                y = ld_io(w.k, bk + t * w.sk[1] + a, p.bf16);
-            }
-            sa[i][a] = x;
-            sk[i][a] = y;
+#pragma unroll
+        for (int u = 0; u < NA; ++u) {
+            const int e = tid + 256 * u;
+            (&sa[0][0])[e] = xa[u];
+            (&sk[0][0])[e] = xk[u];
         }
-        for (int e = tid; e < TT * 32; e += 256) {
-            const int i = e >> 5, c = c0 + (e & 31);
-            float x = 0.f;
-            if (i < m && c < w.dc) {
-                const long long t = w.rev ? n - 1 - i0 - i : i0 + i;
-                x = ld_io(w.v, bv + t * w.sv[1] + c, p.bf16);
-            }
-            sv[i][e & 31] = x * w.write;
-        }
+#pragma unroll
+        for (int u = 0; u < NV; ++u) (&sv[0][0])[tid + 256 * u] = xv[u];
         __syncthreads();
+        if (i0 + TT < n) fetch(i0 + TT);
 #pragma unroll 4
         for (int i = 0; i < m; ++i) {
             const float v = sv[i][lane];
