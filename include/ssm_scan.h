@@ -410,7 +410,8 @@ SSM_API int ssm_cp_write_adjoint(const ssm_desc_t *d, const void *x, const void 
  * ---- The layer around the mixer ------------------------------------------------------
  * Operators a layer needs next to its scan.  They take their own small descriptors;
  * strides are element strides, the innermost dimension of every tensor is dense, inputs
- * may be broadcast (stride 0), outputs may not.  Caller-owned memory, the caller's
+ * may be broadcast (stride 0), outputs may not, and an output overlaps no input unless its
+ * call says so.  Caller-owned memory, the caller's
  * stream and the error codes of the calls above; the descriptors' reserved fields must
  * be 0.  Nothing is launched for an empty problem (no rows, batch or tokens) except
  * where a call says what it then writes.
@@ -528,8 +529,8 @@ SSM_API int ssm_rope_bwd(const ssm_rope_desc_t *d, const void *dq, const void *d
  *   v, dv   [batch][seqlen][nheads_kv][dim_v]    o, do   [batch][seqlen][nheads][dim_v]
  *   states  fp32 [batch][nheads][dim_k][dim_v], dense;  log_decay fp32 [nheads], <= 0
  * (-inf keeps nothing).  lengths (int32 [batch] on the device, NULL: all seqlen) ends row b
- * after its first lengths[b] tokens (clamped to 0 .. seqlen): the rows behind them are not
- * read, and those of the outputs are left as they were.  dim_k and dim_v up to 256.
+ * after its first lengths[b] tokens (clamped to 0 .. seqlen): the rows behind them count for
+ * nothing, whatever they hold, and those of the outputs are left as they were.  dim_k and dim_v up to 256.
  * The decays are constants of the head and have no gradient; a learned, per-token
  * decay is ssm_scan_*.  A value that is not finite in a token of the sequence may reach every
  * output of its batch row and head.
@@ -545,9 +546,10 @@ typedef struct ssm_linattn_desc {
 } ssm_linattn_desc_t;
 
 /* SSM_LINATTN_AUTO: the tensor-core walk over 128-token chunks where it applies (bf16,
- * head dims that are multiples of 8 and at most 128, 16-byte aligned tensors and strides,
- * and more than 1024 / head dim tokens), else the token-by-token recurrence; SSM_LINATTN_RECURRENT: always the latter.  Results
- * are equal up to rounding. */
+ * head dims that are multiples of 8, dim_k at most 128 and for the gradient dim_v too, 16-byte
+ * aligned tensors and strides, and more than 1024 / max(dim_k, dim_v) tokens), else the
+ * token-by-token recurrence; SSM_LINATTN_RECURRENT: always the latter.  Results are equal up
+ * to rounding. */
 enum ssm_linattn_route { SSM_LINATTN_AUTO = 0, SSM_LINATTN_RECURRENT = 1 };
 
 /* Bytes of device workspace (256-byte aligned, contents arbitrary) that ssm_linattn_fwd
@@ -569,8 +571,8 @@ SSM_API int ssm_linattn_fwd(const ssm_linattn_desc_t *d, const void *q, const vo
  *     token: e^{g} G = dstate_out),   dk_t = G_t v_t,   dv_t = G_t^T k_t,
  *     dstate_in = e^{g} G_0
  * The states are recomputed; dk and dv sum the heads that share them in a fixed order.
- * dq, dk and dv are written up to each row's length.  dstate_in may be NULL; it must not be
- * dstate_out, which two of the sums read.
+ * dq, dk and dv are written up to each row's length.  dstate_in may be NULL; it must be
+ * neither dstate_out nor state_in, which other sums of the call read.
  */
 SSM_API int ssm_linattn_bwd(const ssm_linattn_desc_t *d, const void *q, const void *k,
                             const void *v, const float *log_decay, const float *state_in,

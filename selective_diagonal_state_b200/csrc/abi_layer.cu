@@ -66,12 +66,21 @@ int check_stride(const char *name, int64_t stride, int64_t extent, int64_t inner
 }
 int check_strides3(const char *name, const int64_t *s, const int64_t *extent, int64_t inner,
                    bool written) {
+    int order[3], n = 0;   // the dimensions with more than one entry, the smallest stride first
     for (int i = 0; i < 3; ++i) {
         const int rc = check_stride(name, s[i], extent[i], inner, written);
         if (rc) return rc;
-        for (int j = 0; written && j < i; ++j)
-            if (extent[i] > 1 && extent[j] > 1 && s[i] == s[j])
-                return fail(SSM_ERR_ARG, "%s: two dimensions have stride %lld", name, (long long)s[i]);
+        if (extent[i] < 2) continue;
+        int j = n++;
+        for (; j > 0 && s[order[j - 1]] > s[i]; --j) order[j] = order[j - 1];
+        order[j] = i;
+    }
+    // what is written is nested: each dimension steps over all that the smaller ones span
+    double span = (double)inner;
+    for (int j = 0; written && j < n; ++j) {
+        if ((double)s[order[j]] < span)
+            return fail(SSM_ERR_ARG, "%s: stride %lld overlaps other rows", name, (long long)s[order[j]]);
+        span += (double)s[order[j]] * (double)(extent[order[j]] - 1);
     }
     return SSM_OK;
 }
@@ -128,7 +137,7 @@ int rope(const char *where, const ssm_rope_desc_t *d, const void *q, const void 
         (has_k && (rc = check_strides3("k_out", d->stride_k_out, ek, d->headdim, true))))
         return rc;
     if (d->stride_pos[0] < 0 || d->stride_pos[1] < 0) return fail(SSM_ERR_ARG, "negative stride");
-    if (d->batch == 0 || d->seqlen == 0) return SSM_OK;
+    if (d->batch == 0 || d->seqlen == 0 || (d->nheads_q == 0 && d->nheads_k == 0)) return SSM_OK;
     if (!q && !k) return fail(SSM_ERR_ARG, "q and k are both NULL");
     const size_t es = esize(d->dtype_io);
     if ((has_q && ((rc = need(q, "q", es)) || (rc = need(q_out, "q_out", es)))) ||
@@ -403,11 +412,12 @@ int ssm_linattn_fwd(const ssm_linattn_desc_t *d, const void *q, const void *k, c
     if (rc) return rc;
     const int64_t eh[3] = {d->batch, d->seqlen, d->nheads};
     if (o && (rc = check_strides3("o", d->stride_o, eh, d->dim_v, true))) return rc;
-    if (!o && !state_out) return fail(SSM_ERR_ARG, "o and state_out are both NULL");
+    const bool empty = d->batch == 0 || d->seqlen == 0;
+    if (!o && !state_out && !empty) return fail(SSM_ERR_ARG, "o and state_out are both NULL");
     if ((rc = may(state_in, "state_in", 4)) || (rc = may(state_out, "state_out", 4)) ||
         (rc = may(lengths, "lengths", 4)) || (rc = may(o, "o", esize(d->dtype_io))))
         return rc;
-    if (d->batch == 0 || d->seqlen == 0)
+    if (empty)
         return launched("ssm_linattn_fwd (empty)", stream,
                         [&](cudaStream_t st) { return state_copy(state_out, state_in, d, st); });
     if ((rc = la_inputs(d, q, k, v, log_decay))) return rc;
@@ -436,8 +446,8 @@ int ssm_linattn_bwd(const ssm_linattn_desc_t *d, const void *q, const void *k, c
     if ((rc = may(state_in, "state_in", 4)) || (rc = may(dstate_out, "dstate_out", 4)) ||
         (rc = may(dstate_in, "dstate_in", 4)) || (rc = may(lengths, "lengths", 4)))
         return rc;
-    if (dstate_in && dstate_in == dstate_out)
-        return fail(SSM_ERR_ARG, "dstate_in must not be dstate_out");
+    if (dstate_in && (dstate_in == dstate_out || dstate_in == state_in))
+        return fail(SSM_ERR_ARG, "dstate_in must be neither dstate_out nor state_in");
     if (d->batch == 0 || d->seqlen == 0)
         return launched("ssm_linattn_bwd (empty)", stream,
                         [&](cudaStream_t st) { return state_copy(dstate_in, dstate_out, d, st); });

@@ -125,6 +125,8 @@ def _workspace(p, given):
     if given is not None:
         if given.get_device() != p.dev:
             raise ValueError("the workspace must live on the tensors' device")
+        if not given.is_contiguous():
+            raise ValueError("the workspace must be contiguous")
         return given.data_ptr(), given.numel() * given.element_size(), given
     if p.ws == 0:
         return None, 0, None
@@ -227,6 +229,7 @@ def rmsnorm(x, weight=None, residual=None, eps=1e-5, quant=None, want_y=None, wa
     ``quant``: None, "row" or "block" (128 columns) for e4m3 codes with scales; ``want_y``: also
     the unquantised norm (default: only without ``quant``); ``want_rstd`` for a later
     :func:`rmsnorm_backward`; ``r``: where the sum goes (may be ``x`` or ``residual``)."""
+    eps = float(eps)
     p = _plan(("norm", _sig(x), _sig(weight), _sig(residual), _sig(r), eps, quant, want_y),
               _norm_fwd_plan, x, weight, residual, r, eps, quant, want_y)
     return _on_device(_norm_fwd, p, stream, x, weight, residual, r, want_rstd)
@@ -339,6 +342,7 @@ def rope(q, k, freq, positions=None, layout="half", magnitude=1.0, q_out=None, k
     q, k: [batch, seqlen, heads, headdim] (either may be None); ``freq`` from
     :func:`rope_frequencies`; ``positions``: int64 [batch, seqlen] or [seqlen] (default 0, 1, ...);
     ``layout``: "half" pairs value i with i + rot / 2, "pairs" neighbours; outputs may be the inputs."""
+    magnitude = float(magnitude)
     p = _plan(("rope", _sig(q), _sig(k), _sig(freq), _sig(positions), layout, magnitude, _sig(q_out), _sig(k_out)),
               _rope_plan, q, k, freq, positions, layout, magnitude, q_out, k_out)
     return _on_device(_rope, p, stream, False, q, k, freq, positions, q_out, k_out)
@@ -347,6 +351,7 @@ def rope(q, k, freq, positions=None, layout="half", magnitude=1.0, q_out=None, k
 def rope_backward(dq, dk, freq, positions=None, layout="half", magnitude=1.0, dq_out=None,
                   dk_out=None, stream=None):
     """Gradients of :func:`rope`'s inputs for those of its outputs."""
+    magnitude = float(magnitude)
     p = _plan(("rope", _sig(dq), _sig(dk), _sig(freq), _sig(positions), layout, magnitude, _sig(dq_out), _sig(dk_out)),
               _rope_plan, dq, dk, freq, positions, layout, magnitude, dq_out, dk_out)
     return _on_device(_rope, p, stream, True, dq, dk, freq, positions, dq_out, dk_out)
@@ -411,8 +416,9 @@ def linattn(q, k, v, log_decay, scale=None, state=None, lengths=None, out=None, 
 
     q [B, L, H, dim_k], k [B, L, G, dim_k], v [B, L, G, dim_v] with H a multiple of G;
     ``scale`` defaults to dim_k ** -0.5; ``state`` fp32 [B, H, dim_k, dim_v] enters (default
-    zero); ``lengths`` int32 [B]: rows behind them are neither read nor written (``out``
+    zero); ``lengths`` int32 [B]: rows behind them count for nothing and are not written (``out``
     keeps them).  ``state_out`` takes the final state (may be ``state``)."""
+    scale = None if scale is None else float(scale)
     p = _plan(("la", _sig(q), _sig(k), _sig(v), _sig(log_decay), scale, _sig(state), _sig(lengths), _sig(out),
                _sig(state_out), route),
               _la_fwd_plan, q, k, v, log_decay, scale, state, lengths, out, state_out, route)
@@ -448,6 +454,7 @@ def linattn_backward(q, k, v, log_decay, do, scale=None, state=None, dstate=None
     final state (default zero); the returned dstate is that of the entering ``state``.
     ``out``: buffers (dq, dk, dv), whose rows behind ``lengths`` stay as they are."""
     dq, dk, dv = out if out is not None else (None, None, None)
+    scale = None if scale is None else float(scale)
     p = _plan(("la'", _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(do), scale, _sig(state), _sig(dstate),
                _sig(lengths), _sig(dq), _sig(dk), _sig(dv), route),
               _la_bwd_plan, q, k, v, log_decay, do, scale, state, dstate, lengths, dq, dk, dv, route)
@@ -471,6 +478,7 @@ def _la_step(p, st, q, k, v, log_decay, state, out):
 
 def linattn_step(q, k, v, log_decay, state, scale=None, out=None, stream=None):
     """o [B, 1, H, dim_v] of one token (seqlen 1); ``state`` is updated in place."""
+    scale = None if scale is None else float(scale)
     p = _plan(("la1", _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(state), scale, _sig(out)),
               _la_step_plan, q, k, v, log_decay, state, scale, out)
     return _on_device(_la_step, p, stream, q, k, v, log_decay, state, out)

@@ -223,6 +223,33 @@ def test_linattn_stride_refusals(lib):
         assert lib.ssm_linattn_workspace_size(d, abi.PASS_BWD) == 0 and "negative" in err(lib)
 
 
+def test_outputs_that_overlap_are_refused(lib):
+    """Written rows are nested in some order of the dimensions; any order is taken."""
+    d = la_desc()       # [2, 8, 4, 64]
+    d.stride_o[:] = 8 * 64, 64, 2 * 8 * 64       # [H, B, L, 64]
+    d.stride_dq[:] = 64, 2 * 64, 2 * 8 * 64      # [H, L, B, 64]
+    assert lib.ssm_linattn_fwd(d, *[FAKE] * 3, None, *[FAKE] * 4, None, 0, None) == -1 and "log_decay" in err(lib)
+    d.stride_o[:] = 8 * 4 * 64, 64, 3 * 64       # the heads of a token over the next tokens
+    assert lib.ssm_linattn_fwd(d, *[FAKE] * 8, None, 0, None) == -1 and "overlaps" in err(lib)
+    d.stride_o[:] = 7 * 4 * 64, 4 * 64, 64       # a batch row over the end of the one before
+    assert lib.ssm_linattn_fwd(d, *[FAKE] * 8, None, 0, None) == -1 and "overlaps" in err(lib)
+    r = rope_desc()
+    r.stride_k_out[:] = 8 * 2 * 64 - 8, 2 * 64, 64
+    assert lib.ssm_rope_fwd(r, *[FAKE] * 6, None) == -1 and "k_out" in err(lib)
+
+
+def test_states_of_the_gradient_may_not_be_shared(lib):
+    d = la_desc(g=4)
+    args = dict.fromkeys(["q", "k", "v", "log_decay", "state_in", "lengths", "do", "dstate_out", "dq", "dk", "dv"], FAKE)
+    args["state_in"] = FAKE + 256
+    assert lib.ssm_linattn_bwd(d, *args.values(), FAKE + 256, None, 0, None) == -1 and "state_in" in err(lib)
+
+
+def test_nothing_to_do_is_no_error(lib):
+    assert lib.ssm_linattn_fwd(la_desc(seqlen=0), *[None] * 8, None, 0, None) == 0
+    assert lib.ssm_rope_fwd(rope_desc(hq=0, hk=0), *[None] * 6, None) == 0
+
+
 def test_host_tensors_refused():
     torch = pytest.importorskip("torch")
     from selective_diagonal_state_b200 import layer

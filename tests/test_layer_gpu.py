@@ -404,6 +404,121 @@ def test_linattn_empty_and_in_place(layer):
     assert (o5[0] == 3.0).all() and torch.equal(o5[1], o1[1]) and torch.equal(S5[0], S[0]) and torch.equal(S5[1], S1[1])
 
 
+def state_only(q, k, v, dec, state, lengths, route=abi.LINATTN_AUTO):
+    """The final state by the C call without an output."""
+    B, L, H, dk = q.shape
+    d = abi.LinattnDesc(batch=B, seqlen=L, nheads=H, nheads_kv=k.shape[2], dim_k=dk, dim_v=v.shape[3], scale=1.0,
+                        dtype_io=abi.DTYPE_BF16 if q.dtype == torch.bfloat16 else abi.DTYPE_F32, route=route)
+    for name, x in (("q", q), ("k", k), ("v", v), ("o", q), ("dq", q), ("dk", k), ("dv", v)):
+        getattr(d, "stride_" + name)[:] = x.stride()[:3]
+    n = abi.ssm_linattn_workspace_size(d, abi.PASS_FWD)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    out = torch.empty(B, H, dk, v.shape[3], device="cuda")
+    p = lambda x: None if x is None else x.data_ptr()  # noqa: E731
+    rc = abi.load_library().ssm_linattn_fwd(d, p(q), p(k), p(v), p(dec), p(state), p(lengths), None, p(out), p(ws), n,
+                                            torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    return out
+
+
+@pytest.mark.parametrize("t,L,dk,dv,ragged", [("bf16", 7, 64, 64, False), ("bf16", 300, 64, 128, True),
+                                              ("bf16", 2600, 64, 64, True), ("fp32", 41, 20, 36, True)])
+def test_linattn_state_only_and_in_place(layer, t, L, dk, dv, ragged):
+    """Without an output, and with the state updated in place, the state is that of the whole
+    call, bit by bit, however the sequence is split."""
+    T, _ = la_case(L, t, 3, L, 2, 1, dk, dv, ragged)
+    args = [T[x] for x in ("q", "k", "v", "log_decay")]
+    _, S = layer.linattn(*args, state=T["state"], lengths=T["lengths"])
+    assert torch.equal(state_only(*args, T["state"], T["lengths"]), S)
+    here = T["state"].clone()
+    layer.linattn(*args, state=here, state_out=here, lengths=T["lengths"])
+    assert torch.equal(here, S)
+
+
+def test_linattn_long_ragged(layer):
+    """Sequences long and few enough to be split, that end anywhere in a split."""
+    T, N = la_case(33, "bf16", 4, 2600, 2, 1, 64, 64, True)
+    N["lengths"] = np.array([0, 1, 1279, 2600])
+    T["lengths"] = torch.from_numpy(N["lengths"].astype(np.int32)).cuda()
+    for name in ("q", "k", "v", "do"):
+        for b, n in enumerate(N["lengths"]):
+            T[name][b, :n] = torch.from_numpy(N[name][b, :n]).to(T[name])
+            T[name][b, n:] = float("nan")
+    la_check(layer, T, N, "bf16", 0.125, True)
+
+
+def test_rows_far_apart(layer):
+    """Batch rows more than 2^31 values apart."""
+    far = (1 << 31) + 64
+    big = torch.empty(far + 300 * 256, dtype=torch.bfloat16, device="cuda")
+    T, _ = la_case(5, "bf16", 2, 300, 1, 1, 64, 64, False)
+
+    def spread(x, at):
+        y = big.as_strided((2, 300, 1, 64), (far, 256, 64, 1), at)
+        y.copy_(x)
+        return y
+    q, k, v, do = (spread(T[x], 64 * i) for i, x in enumerate(("q", "k", "v", "do")))
+    dec = T["log_decay"]
+    for route in (abi.LINATTN_AUTO, abi.LINATTN_RECURRENT):
+        near = layer.linattn(T["q"], T["k"], T["v"], dec, route=route)
+        assert all(torch.equal(a, b) for a, b in zip(near, layer.linattn(q, k, v, dec, route=route)))
+        near = layer.linattn_backward(T["q"], T["k"], T["v"], dec, T["do"], route=route)
+        assert all(torch.equal(a, b) for a, b in zip(near, layer.linattn_backward(q, k, v, dec, do, route=route)))
+    freq = layer.rope_frequencies(64)
+    assert all(torch.equal(a, b) for a, b in zip(layer.rope(T["q"], T["k"], freq), layer.rope(q, k, freq)))
+    x, y = T["q"].reshape(2, -1)[:, :512].contiguous(), big.as_strided((2, 512), (far, 1), 0)
+    y.copy_(x)
+    a, b = layer.rmsnorm(x, want_rstd=True), layer.rmsnorm(y, want_rstd=True)
+    assert torch.equal(a.y, b.y)
+    c = layer.rmsnorm_backward(x, y, None, b.rstd, dx=big.as_strided((2, 512), (far, 1), 1024))[0]
+    assert torch.equal(c, layer.rmsnorm_backward(x, x, None, a.rstd)[0])
+    wide = layer.rope(T["q"], None, freq, q_out=q)[0]
+    assert torch.equal(wide, layer.rope(T["q"], None, freq)[0])
+    layer.linattn(T["q"], T["k"], T["v"], dec, out=q)
+    assert torch.equal(q, layer.linattn(T["q"], T["k"], T["v"], dec)[0])
+
+
+def test_numbers_given_as_tensors_are_read_every_call(layer):
+    """A factor that lives in a tensor is its value at the call, not at the first one."""
+    g = np.random.default_rng(3)
+    q, _ = draw(g, (1, 4, 2, 16), "fp32")
+    dec = torch.tensor([-0.1, -0.2], device="cuda")
+    s, e = torch.tensor(0.5), torch.tensor(1e-5)
+    a = layer.linattn(q, q, q, dec, scale=s)[0]
+    n = layer.rmsnorm(q, eps=e).y
+    s.fill_(1.0)
+    e.fill_(10.0)
+    assert torch.equal(layer.linattn(q, q, q, dec, scale=s)[0], 2 * a)
+    assert not torch.equal(layer.rmsnorm(q, eps=e).y, n)
+
+
+def test_helpers_refuse(layer):
+    q = torch.zeros(2, 200, 4, 64, dtype=torch.bfloat16, device="cuda")
+    dec = torch.zeros(4, device="cuda")
+    few = torch.empty(2, 200 * 4 * 64 * 8 * 2, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        layer.linattn_backward(q, q[:, :, :2], q[:, :, :2], dec, q, workspace=few[:, ::2])
+    with pytest.raises(abi.SsmError, match="workspace"):
+        layer.linattn_backward(q, q[:, :, :2], q[:, :, :2], dec, q, workspace=few[0, :256])
+    with pytest.raises(ValueError, match="device"):
+        layer.linattn_backward(q, q, q, dec, q, workspace=torch.empty(8, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="type"):
+        layer.linattn(q, q.float(), q, dec)
+    with pytest.raises(ValueError, match="shape"):
+        layer.linattn(q, q, q, dec[:3])
+    with pytest.raises(ValueError, match="contiguous"):
+        layer.linattn(q, q, q, dec, state=torch.zeros(2, 4, 64, 128, device="cuda")[..., ::2])
+    with pytest.raises(abi.SsmError, match="overlaps"):
+        layer.linattn(q, q, q, dec, out=q[:1].expand(2, -1, -1, -1))
+    with pytest.raises(ValueError, match="evenly"):
+        layer.rmsnorm(q.transpose(0, 1))
+    with pytest.raises(ValueError, match="quant"):
+        layer.rmsnorm(q, quant="tensor")
+    z = q[:, :0]
+    o, s = layer.linattn(z, z, z, dec, want_state=False)      # nothing to write is no error
+    assert o.shape == z.shape and s is None
+
+
 # ---- together --------------------------------------------------------------------------
 
 def _block(layer, x, res, w, proj, freq, pos, dec, state=None, step=False):
