@@ -2,10 +2,12 @@
 // rotation): pair j of every head at position m turns by m freq[j],
 //     (a, b) -> magnitude (a cos - b sin, a sin + b cos).
 // The angle is taken in 64 bits, in half turns, and reduced to (-1, 1] there, so that
-// sincospi of its fp32 rest is right for any position.  Bound by memory (each value read
-// and written once): a thread takes one 16-byte piece of pairs of a token (two pieces in
-// the half layout) and turns it for all, or a share of, the heads of q and k with one
-// set of sines; the values past rot_dim are copied piece by piece.
+// sincospi of its fp32 rest is right for any position.  Bound by memory, each value read and
+// written once, as long as the rest is kept small: the 64-bit steps of an angle are taken
+// once a block, a thread keeps a piece's sines and its addresses for up to eight heads, and has
+// four of them on their way.  On one B200, 65536 tokens of 32 heads of 128 (bf16, all
+// of a head turned): 165 us, 6.5 TB/s; with two heads on their way 173, with four heads a
+// thread 211, with the angles taken by every thread that needs them 190.
 #include "common.cuh"
 #include "layer.h"
 
@@ -22,6 +24,7 @@ struct RopeArgs {
     int L, hq, hk, dim, rot;
     int units;          // pieces a token: rotated ones, then copied ones
     int urot, share;    // rotated pieces; threads that share the heads of a piece
+    int per_block;      // tokens of a block
     int pairs;          // layout (2 i, 2 i + 1)
     float mag, sign;
 };
@@ -35,6 +38,9 @@ __device__ __forceinline__ void turn(double angle_halfturns, float mag, float si
     s = mag * sign * sn;
 }
 
+constexpr int TURNS = 4096;   // pairs whose sines a block may hold
+constexpr int EACH = 8;       // heads a thread turns at most
+constexpr int NB = 4;         // of which it has so many on their way at once
 constexpr double INV_PI = 0.31830988618379067154;
 
 template <bool BF16> __device__ __forceinline__ void unpack(const uint4 &w, float *v) {
@@ -63,63 +69,84 @@ template <bool BF16> __device__ __forceinline__ uint4 pack(const float *v) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// Pieces of N values (16 bytes): dense and 16-byte aligned heads.
+// Pieces of N values (16 bytes): dense and 16-byte aligned heads.  A block takes p.per_block
+// tokens: its threads first take the sines of all their pairs, one each, into shared
+// memory, then turn the pieces, a thread the same piece of some of the token's heads.
 template <bool BF16, bool PAIRS>
 __global__ void __launch_bounds__(256) k_rope(const RopeArgs p) {
     constexpr int N = BF16 ? 8 : 4, ES = 16 / N, NP = PAIRS ? N / 2 : N;
-    const long long per_token = (long long)p.units * p.share;
-    const long long id = blockIdx.x * 256ll + threadIdx.x;
-    const long long tok = id / per_token;
-    if (tok >= p.tokens) return;
-    const int rest = (int)(id - tok * per_token);
-    const int h0 = rest / p.units, u = rest - h0 * p.units;
-    const long long b = tok / p.L, t = tok - b * p.L;
-    const bool rotated = u < p.urot;
-    float c[NP], s[NP];
-    if (rotated) {
-        const double m = p.pos ? (double)p.pos[b * p.sp[0] + t * p.sp[1]] : (double)t;
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-            turn(m * (p.freq[u * NP + i] * INV_PI), p.mag, p.sign, c[i], s[i]);
+    extern __shared__ float2 turns[];   // [token of the block][pair] (cosine, sine)
+    const int tid = threadIdx.x, np = p.rot / 2;
+    const long long t0 = (long long)blockIdx.x * p.per_block, b0 = t0 / p.L;
+    const uint32_t first = (uint32_t)(t0 - b0 * p.L);   // the block's first token in its batch row
+    const int nt = (int)min((long long)p.per_block, p.tokens - t0), items = nt * p.units * p.share;
+    for (int i = tid; i < nt * np; i += 256) {
+        const int l = i / np;
+        const uint32_t at = first + l, rows = at / p.L, t = at - rows * p.L;
+        const double m = p.pos ? (double)p.pos[(b0 + rows) * p.sp[0] + t * p.sp[1]] : (double)t;
+        float2 w;
+        turn(m * (p.freq[i - l * np] * INV_PI), p.mag, p.sign, w.x, w.y);
+        turns[i] = w;
     }
-    // first value of the piece in its head, and of its partner in the half layout
-    const int e0 = rotated ? u * N : p.rot + (u - p.urot) * N, e1 = e0 + p.rot / 2;
-    const int heads = p.hq + p.hk;
-#pragma unroll 4
-    for (int hh = h0; hh < heads; hh += p.share) {
-        const bool isk = hh >= p.hq;
-        const int h = isk ? hh - p.hq : hh;
-        const long long *si = isk ? p.sk : p.sq, *so = isk ? p.sko : p.sqo;
-        const char *in = reinterpret_cast<const char *>(isk ? p.k : p.q) +
-                         (b * si[0] + t * si[1] + h * si[2] + e0) * ES;
-        char *out = reinterpret_cast<char *>(isk ? p.ko : p.qo) +
-                    (b * so[0] + t * so[1] + h * so[2] + e0) * ES;
-        const uint4 w = *reinterpret_cast<const uint4 *>(in);
-        if (!rotated) {
-            *reinterpret_cast<uint4 *>(out) = w;
-            continue;
-        }
-        float x[N];
-        unpack<BF16>(w, x);
-        if (PAIRS) {
+    __syncthreads();
+    for (int e = tid; e < items; e += 256) {
+        const int u = e % p.units, r = e / p.units, tl = r / p.share;
+        int h = r - tl * p.share;
+        const uint32_t at = first + tl, rows = at / p.L, t = at - rows * p.L;
+        const long long b = b0 + rows;
+        const bool rotated = u < p.urot;
+        const int e0 = rotated ? u * N : p.rot + (u - p.urot) * N;
+        const int across = np * ES;   // bytes from a piece to its partner in the half layout
+        float2 w[NP];
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const float a = x[2 * i], bb = x[2 * i + 1];
-                x[2 * i] = a * c[i] - bb * s[i];
-                x[2 * i + 1] = a * s[i] + bb * c[i];
-            }
-        } else {
-            float y[N];
-            unpack<BF16>(*reinterpret_cast<const uint4 *>(in + (e1 - e0) * ES), y);
+        for (int i = 0; i < NP; ++i) w[i] = rotated ? turns[tl * np + (PAIRS ? e0 / 2 : e0) + i] : make_float2(1.f, 0.f);
+        // q's heads, then k's
+#pragma unroll 1
+        for (int op = 0; op < 2; ++op) {
+            const int n = op ? p.hk : p.hq;
+            const long long *si = op ? p.sk : p.sq, *so = op ? p.sko : p.sqo;
+            const char *in = reinterpret_cast<const char *>(op ? p.k : p.q) + (b * si[0] + t * si[1] + h * si[2] + e0) * ES;
+            char *out = reinterpret_cast<char *>(op ? p.ko : p.qo) + (b * so[0] + t * so[1] + h * so[2] + e0) * ES;
+            const long long di = p.share * si[2] * ES, dn = p.share * so[2] * ES;
+#pragma unroll 1
+            for (; h < n; h += NB * p.share) {
+                uint4 lo[NB], hi[NB];
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const float a = x[i], bb = y[i];
-                x[i] = a * c[i] - bb * s[i];
-                y[i] = a * s[i] + bb * c[i];
+                for (int i = 0; i < NB; ++i, in += di) {
+                    if (h + i * p.share >= n) continue;
+                    lo[i] = *reinterpret_cast<const uint4 *>(in);
+                    if (!PAIRS && rotated) hi[i] = *reinterpret_cast<const uint4 *>(in + across);
+                }
+#pragma unroll
+                for (int i = 0; i < NB; ++i, out += dn) {
+                    if (h + i * p.share >= n) continue;
+                    if (rotated) {
+                        float x[N], y[N];
+                        unpack<BF16>(lo[i], x);
+                        if (PAIRS) {
+#pragma unroll
+                            for (int k = 0; k < NP; ++k) {
+                                const float a = x[2 * k], c = x[2 * k + 1];
+                                x[2 * k] = a * w[k].x - c * w[k].y;
+                                x[2 * k + 1] = a * w[k].y + c * w[k].x;
+                            }
+                        } else {
+                            unpack<BF16>(hi[i], y);
+#pragma unroll
+                            for (int k = 0; k < NP; ++k) {
+                                const float a = x[k], c = y[k];
+                                x[k] = a * w[k].x - c * w[k].y;
+                                y[k] = a * w[k].y + c * w[k].x;
+                            }
+                            *reinterpret_cast<uint4 *>(out + across) = pack<BF16>(y);
+                        }
+                        lo[i] = pack<BF16>(x);
+                    }
+                    *reinterpret_cast<uint4 *>(out) = lo[i];
+                }
             }
-            *reinterpret_cast<uint4 *>(out + (e1 - e0) * ES) = pack<BF16>(y);
+            h = (h - n) % p.share;   // k's heads go on where q's end
         }
-        *reinterpret_cast<uint4 *>(out) = pack<BF16>(x);
     }
 }
 
@@ -201,7 +228,7 @@ cudaError_t rope_rotate(const ssm_rope_desc_t &d, const void *q, const void *k, 
     const bool still = in_place(q, q_out, d.stride_q, d.stride_q_out) &&
                        in_place(k, k_out, d.stride_k, d.stride_k_out);
     const int rest = still ? 0 : a.dim - a.rot;
-    vec = vec && a.dim % n == 0 && (a.pairs ? a.rot % n : a.rot % (2 * n)) == 0;
+    vec = vec && a.rot / 2 <= TURNS && a.dim % n == 0 && (a.pairs ? a.rot % n : a.rot % (2 * n)) == 0;
     if (vec) {
         a.urot = a.pairs ? a.rot / n : a.rot / (2 * n);
         a.units = a.urot + rest / n;
@@ -210,18 +237,26 @@ cudaError_t rope_rotate(const ssm_rope_desc_t &d, const void *q, const void *k, 
         a.units = a.urot + rest;
     }
     if (a.units == 0) return cudaSuccess;
-    // share the heads among more threads until the card has a few warps a scheduler
-    a.share = 1;
-    const long long want = (long long)sm_count() * 1024;
-    while (vec && 2 * a.share <= a.hq + a.hk && a.tokens * a.units * a.share < want) a.share *= 2;
-    const long long threads = a.tokens * a.units * a.share;
-    const unsigned grid = (unsigned)((threads + 255) / 256);
-    if (vec && bf16)
-        a.pairs ? k_rope<true, true><<<grid, 256, 0, st>>>(a) : k_rope<true, false><<<grid, 256, 0, st>>>(a);
-    else if (vec)
-        a.pairs ? k_rope<false, true><<<grid, 256, 0, st>>>(a) : k_rope<false, false><<<grid, 256, 0, st>>>(a);
-    else
+    if (!vec) {
+        const unsigned grid = (unsigned)((a.tokens * a.units + 255) / 256);
         bf16 ? k_rope_any<true><<<grid, 256, 0, st>>>(a) : k_rope_any<false><<<grid, 256, 0, st>>>(a);
+        profile_mark(st, "k_rope_any");
+        return cudaGetLastError();
+    }
+    // fewer heads a thread until the card has eight warps a scheduler: 8192 tokens of 27 heads of
+    // 64 took 11.4 us with eight heads a thread and 15.7 with four, 8 tokens of 20 heads of 128 3.9
+    const long long heads = a.hq + a.hk, threads = (long long)sm_count() * 1024;
+    int each = EACH;
+    while (each > 1 && a.tokens * a.units * ((heads + each - 1) / each) < threads) each /= 2;
+    a.share = (int)((heads + each - 1) / each);
+    const long long fit = 256 / ((long long)a.units * a.share), spread = a.tokens / sm_count(), room = TURNS / (a.rot / 2);
+    a.per_block = (int)max(1ll, min(fit, min(spread, room)));
+    const size_t smem = sizeof(float2) * a.per_block * (a.rot / 2);
+    const unsigned grid = (unsigned)((a.tokens + a.per_block - 1) / a.per_block);
+    if (bf16)
+        a.pairs ? k_rope<true, true><<<grid, 256, smem, st>>>(a) : k_rope<true, false><<<grid, 256, smem, st>>>(a);
+    else
+        a.pairs ? k_rope<false, true><<<grid, 256, smem, st>>>(a) : k_rope<false, false><<<grid, 256, smem, st>>>(a);
     profile_mark(st, "k_rope");
     return cudaGetLastError();
 }
