@@ -57,7 +57,11 @@ template <> struct Io<false> {
 };
 
 // the larger of two magnitudes; a NaN stays
-__device__ __forceinline__ float top(float a, float b) { return (b > a || b != b) ? b : a; }
+__device__ __forceinline__ float top(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
 
 __device__ __forceinline__ float code_scale(float amax) {
     // 448 / amax, finite for the smallest blocks; a block of zeros has codes 0
