@@ -547,7 +547,7 @@ typedef struct ssm_linattn_desc {
 
 /* SSM_LINATTN_AUTO: the tensor-core walk over 128-token chunks where it applies (bf16,
  * head dims that are multiples of 8, dim_k at most 128 and for the gradient dim_v too, 16-byte
- * aligned tensors and strides, and more than 1024 / max(dim_k, dim_v) tokens), else the
+ * aligned tensors and strides, and more than 2048 / max(dim_k, dim_v) tokens), else the
  * token-by-token recurrence; SSM_LINATTN_RECURRENT: always the latter.  Results are equal up
  * to rounding. */
 enum ssm_linattn_route { SSM_LINATTN_AUTO = 0, SSM_LINATTN_RECURRENT = 1 };

@@ -260,11 +260,11 @@ LaWs la_layout(const ssm_linattn_desc_t *d, bool bwd) {
         w.total = w.dv + align256(tok * ndv * 4);
     }
     if (d->route != SSM_LINATTN_AUTO) return w;
-    // A block on tensor cores takes 10 us whatever it walks, a token of the recurrence 0.2 to 0.5 us:
-    // on one B200, 4 batch rows of 16 heads of 64 took 5.2 us for 16 tokens by the latter and
-    // 10.4 us by the former, and 9.1 and 10.4 us for 32; heads of 128 8.0 and 10.9 us for 8
-    // tokens, 11.3 and 10.9 us for 16 (the gradient 33 and 26 us).
-    if (d->seqlen * (d->dim_k > d->dim_v ? d->dim_k : d->dim_v) <= 1024) return w;
+    // A block on tensor cores takes 10 us whatever it walks, a token of the recurrence 0.1 to 0.4 us:
+    // on one B200, 4 batch rows of 16 heads of 64 took 6.3 us for 32 tokens by the latter and
+    // 10.5 us by the former, and 10.1 and 10.4 us for 64 (the gradient 12.4 and 17.7, 20.6 and 17.7);
+    // heads of 128 8.9 and 10.9 us for 16 tokens, 14.4 and 10.9 us for 32 (26.4 and 26.0, 40.6 and 25.9).
+    if (d->seqlen * (d->dim_k > d->dim_v ? d->dim_k : d->dim_v) <= 2048) return w;
     const bool bf16 = d->dtype_io == SSM_BF16;
     if (!ssm::la_chunked_sizes(bf16, ndk, ndv) || (bwd && !ssm::la_chunked_sizes(bf16, ndv, ndk))) return w;
     const int sk = (ndk + 63) / 64, sv = (ndv + 63) / 64;   // 64-column slices

@@ -9,6 +9,8 @@
 //     dk_t = G_t v_t                                                walk (v, do, q) in reverse, on G^T
 //     dv_t = G_t^T k_t                                              walk (k, q, do) in reverse, on G
 // and the reverse walks leave lam G_0 = dstate_in, having entered with dstate_out.
+#include <type_traits>
+
 #include "common.cuh"
 #include "layer.h"
 
@@ -23,12 +25,26 @@ __device__ __forceinline__ void decay_pair(float g, float &hi, float &lo) {
     lo = (float)(l - (double)hi);
 }
 
+// a value as it lies in memory, converted only when it is used: a load whose value is
+// converted at once is waited for at once
+template <bool BF16> struct Raw {
+    using T = float;
+    static __device__ __forceinline__ float f(T x) { return x; }
+};
+template <> struct Raw<true> {
+    using T = unsigned short;
+    static __device__ __forceinline__ float f(T x) { return __uint_as_float((uint32_t)x << 16); }
+};
+
 // Columns 32 bx .. of one (batch row, head, walk): lane = column, warp w holds the state rows
 // [w NR, (w + 1) NR) in registers.  TT tokens at a time are staged in shared memory as fp32,
-// then every token costs a warp 3 NR FMAs; the eight warps' partial outputs are added once a tile.
-template <int NR, int TT>
+// the next ones waiting in registers; then every token costs a warp 4 NR FMAs, and the eight
+// warps' partial outputs are added once a tile.  Bound by the latency of a tile's steps.
+template <int NR, int TT, bool BF16>
 __global__ void __launch_bounds__(256) k_la_recurrent(const LaArgs p, int slices) {
     constexpr int DA = 8 * NR;
+    using R = Raw<BF16>;
+    using T = typename R::T;
     __shared__ __align__(16) float sa[TT][DA], sk[TT][DA];
     __shared__ float sv[TT][32], part[TT][8][32];
     const LaWalk w = p.w[blockIdx.y];
@@ -37,6 +53,32 @@ __global__ void __launch_bounds__(256) k_la_recurrent(const LaArgs p, int slices
     const int b = bh / p.H, h = bh - b * p.H;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, col = c0 + lane;
     const int n = p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L;
+    const T *pa = reinterpret_cast<const T *>(w.a) + b * w.sa[0] + (h / w.rep_a) * w.sa[2];
+    const T *pk = reinterpret_cast<const T *>(w.k) + b * w.sk[0] + (h / w.rep_k) * w.sk[2];
+    const T *pv = reinterpret_cast<const T *>(w.v) + b * w.sv[0] + (h / w.rep_v) * w.sv[2];
+    const long long bo = b * w.so[0] + h * w.so[2];
+    constexpr int NA = TT * DA / 256, NV = TT * 32 / 256;
+    T xa[NA], xk[NA], xv[NV];
+    auto fetch = [&](int i0) {
+        const int m = min(TT, n - i0);
+#pragma unroll
+        for (int u = 0; u < NA; ++u) {
+            const int e = tid + 256 * u, i = e / DA, a = e - i * DA;
+            const long long t = w.rev ? n - 1 - i0 - i : i0 + i;
+            const bool on = i < m && a < w.da;
+            xa[u] = xk[u] = 0;
+            if (on && w.o) xa[u] = pa[t * w.sa[1] + a];
+            if (on) xk[u] = pk[t * w.sk[1] + a];
+        }
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            const int e = tid + 256 * u, i = e >> 5, c = c0 + (e & 31);
+            const long long t = w.rev ? n - 1 - i0 - i : i0 + i;
+            xv[u] = 0;
+            if (i < m && c < w.dc) xv[u] = pv[t * w.sv[1] + c];
+        }
+    };
+    if (n > 0) fetch(0);
     float lam, lam_lo;
     decay_pair(p.log_decay[h], lam, lam_lo);
     const long long sbase = (long long)bh * w.da * w.dc;
@@ -47,63 +89,45 @@ __global__ void __launch_bounds__(256) k_la_recurrent(const LaArgs p, int slices
         S[r] = (w.s_in && a < w.da && col < w.dc)
                    ? w.s_in[sbase + (long long)a * w.st_a + (long long)col * w.st_c] : 0.f;
     }
-    const long long ba = b * w.sa[0] + (h / w.rep_a) * w.sa[2];
-    const long long bk = b * w.sk[0] + (h / w.rep_k) * w.sk[2];
-    const long long bv = b * w.sv[0] + (h / w.rep_v) * w.sv[2];
-    const long long bo = b * w.so[0] + h * w.so[2];
-    // the next tile's values wait in registers while this one is walked
-    constexpr int NA = TT * DA / 256, NV = TT * 32 / 256;
-    float xa[NA], xk[NA], xv[NV];
-    auto fetch = [&](int i0) {
-        const int m = min(TT, n - i0);
+    // a token of the tile; `rev`: the decay comes behind it
+    auto token = [&](int i, auto rev) {
+        const float v = sv[i][lane];
+        float o = 0.f;
 #pragma unroll
-        for (int u = 0; u < NA; ++u) {
-            const int e = tid + 256 * u, i = e / DA, a = e - i * DA;
-            const long long t = w.rev ? n - 1 - i0 - i : i0 + i;
-            const bool on = i < m && a < w.da;
-            xa[u] = on && w.o ? ld_io(w.a, ba + t * w.sa[1] + a, p.bf16) : 0.f;
-            xk[u] = on ? ld_io(w.k, bk + t * w.sk[1] + a, p.bf16) : 0.f;
-        }
+        for (int r = 0; r < NR; r += 4) {
+            const float4 k4 = *reinterpret_cast<const float4 *>(&sk[i][warp * NR + r]);
+            const float4 a4 = *reinterpret_cast<const float4 *>(&sa[i][warp * NR + r]);
+            const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, aa[4] = {a4.x, a4.y, a4.z, a4.w};
 #pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            const int e = tid + 256 * u, i = e >> 5, c = c0 + (e & 31);
-            const long long t = w.rev ? n - 1 - i0 - i : i0 + i;
-            xv[u] = i < m && c < w.dc ? ld_io(w.v, bv + t * w.sv[1] + c, p.bf16) * w.write : 0.f;
+            for (int q = 0; q < 4; ++q) {
+                float s = S[r + q];
+                if (!decltype(rev)::value) s = fmaf(lam, s, fmaf(lam_lo, s, kk[q] * v));
+                else s = fmaf(kk[q], v, s);
+                o = fmaf(aa[q], s, o);
+                S[r + q] = decltype(rev)::value ? fmaf(lam, s, lam_lo * s) : s;
+            }
         }
+        part[i][warp][lane] = o;
     };
-    if (n > 0) fetch(0);
     for (int i0 = 0; i0 < n; i0 += TT) {
         const int m = min(TT, n - i0);
-        __syncthreads();
+        // every warp is past the tile before (the barrier in front of its sums)
 #pragma unroll
         for (int u = 0; u < NA; ++u) {
             const int e = tid + 256 * u;
-            (&sa[0][0])[e] = xa[u];
-            (&sk[0][0])[e] = xk[u];
+            (&sa[0][0])[e] = R::f(xa[u]);
+            (&sk[0][0])[e] = R::f(xk[u]);
         }
 #pragma unroll
-        for (int u = 0; u < NV; ++u) (&sv[0][0])[tid + 256 * u] = xv[u];
+        for (int u = 0; u < NV; ++u) (&sv[0][0])[tid + 256 * u] = R::f(xv[u]) * w.write;
         __syncthreads();
         if (i0 + TT < n) fetch(i0 + TT);
+        if (w.rev) {
 #pragma unroll 4
-        for (int i = 0; i < m; ++i) {
-            const float v = sv[i][lane];
-            float o = 0.f;
-#pragma unroll
-            for (int r = 0; r < NR; r += 4) {
-                const float4 k4 = *reinterpret_cast<const float4 *>(&sk[i][warp * NR + r]);
-                const float4 a4 = *reinterpret_cast<const float4 *>(&sa[i][warp * NR + r]);
-                const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, aa[4] = {a4.x, a4.y, a4.z, a4.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float s = S[r + q];
-                    if (!w.rev) s = fmaf(lam, s, fmaf(lam_lo, s, kk[q] * v));
-                    else s = fmaf(kk[q], v, s);
-                    o = fmaf(aa[q], s, o);
-                    S[r + q] = w.rev ? fmaf(lam, s, lam_lo * s) : s;
-                }
-            }
-            part[i][warp][lane] = o;
+            for (int i = 0; i < m; ++i) token(i, std::true_type{});
+        } else {
+#pragma unroll 4
+            for (int i = 0; i < m; ++i) token(i, std::false_type{});
         }
         __syncthreads();
         if (w.o)
@@ -114,7 +138,7 @@ __global__ void __launch_bounds__(256) k_la_recurrent(const LaArgs p, int slices
 #pragma unroll
                 for (int q = 1; q < 8; ++q) o += part[i][q][c];
                 const long long t = w.rev ? n - 1 - i0 - i : i0 + i;
-                st_io(w.o, bo + t * w.so[1] + c0 + c, o * w.read, p.bf16 && !w.o_f32);
+                st_io(w.o, bo + t * w.so[1] + c0 + c, o * w.read, BF16 && !w.o_f32);
             }
     }
     if (w.s_out && col < w.dc)
@@ -269,10 +293,11 @@ cudaError_t la_recurrent(const LaArgs &p, cudaStream_t st) {
     }
     const int slices = (dc + 31) / 32;
     const dim3 grid((unsigned)((long long)p.B * p.H * slices), p.nwalk);
-    if (da <= 32) k_la_recurrent<4, 16><<<grid, 256, 0, st>>>(p, slices);
-    else if (da <= 64) k_la_recurrent<8, 16><<<grid, 256, 0, st>>>(p, slices);
-    else if (da <= 128) k_la_recurrent<16, 16><<<grid, 256, 0, st>>>(p, slices);
-    else k_la_recurrent<32, 8><<<grid, 256, 0, st>>>(p, slices);
+    auto go = [&](auto kern) { kern<<<grid, 256, 0, st>>>(p, slices); };
+    if (da <= 32) p.bf16 ? go(k_la_recurrent<4, 16, true>) : go(k_la_recurrent<4, 16, false>);
+    else if (da <= 64) p.bf16 ? go(k_la_recurrent<8, 16, true>) : go(k_la_recurrent<8, 16, false>);
+    else if (da <= 128) p.bf16 ? go(k_la_recurrent<16, 16, true>) : go(k_la_recurrent<16, 16, false>);
+    else p.bf16 ? go(k_la_recurrent<32, 8, true>) : go(k_la_recurrent<32, 8, false>);
     profile_mark(st, "k_la_recurrent");
     return cudaGetLastError();
 }
