@@ -36,17 +36,20 @@ template <> struct Raw<true> {
     static __device__ __forceinline__ float f(T x) { return __uint_as_float((uint32_t)x << 16); }
 };
 
-// Columns 32 bx .. of one (batch row, head, walk): lane = column, warp w holds the state rows
+// Columns 32 bx .. of one (batch row, head, walk): lane = column, warp w of W holds the state rows
 // [w NR, (w + 1) NR) in registers.  TT tokens at a time are staged in shared memory as fp32,
-// the next ones waiting in registers; then every token costs a warp 4 NR FMAs, and the eight
-// warps' partial outputs are added once a tile.  Bound by the latency of a tile's steps.
-template <int NR, int TT, bool BF16>
-__global__ void __launch_bounds__(256) k_la_recurrent(const LaArgs p, int slices) {
-    constexpr int DA = 8 * NR;
+// the next ones waiting in registers; then every token costs a warp 4 NR FMAs, and the W
+// warps' partial outputs are added once a tile.  Bound by the latency of a
+// token's steps and, for wide heads, by shared memory, which gives every lane all of k and a: on
+// one B200, a token costs 0.075 us for heads of 16, 0.11 for 64 and 0.2 for 128 (fp32, 2 x 300 tokens of
+// 4 heads of 16 / 24: 25 us; 2 x 2048 of 8 heads of 64: 227 us; tiles of 16 tokens: 29 and 246).
+template <int NR, int TT, bool BF16, int W = 8>
+__global__ void __launch_bounds__(32 * W) k_la_recurrent(const LaArgs p, int slices) {
+    constexpr int DA = W * NR, THREADS = 32 * W;
     using R = Raw<BF16>;
     using T = typename R::T;
     __shared__ __align__(16) float sa[TT][DA], sk[TT][DA];
-    __shared__ float sv[TT][32], part[TT][8][32];
+    __shared__ float sv[TT][32], part[TT][W][32];
     const LaWalk w = p.w[blockIdx.y];
     const int bh = blockIdx.x / slices, c0 = 32 * (blockIdx.x - bh * slices);
     if (c0 >= w.dc) return;
@@ -57,13 +60,13 @@ __global__ void __launch_bounds__(256) k_la_recurrent(const LaArgs p, int slices
     const T *pk = reinterpret_cast<const T *>(w.k) + b * w.sk[0] + (h / w.rep_k) * w.sk[2];
     const T *pv = reinterpret_cast<const T *>(w.v) + b * w.sv[0] + (h / w.rep_v) * w.sv[2];
     const long long bo = b * w.so[0] + h * w.so[2];
-    constexpr int NA = TT * DA / 256, NV = TT * 32 / 256;
+    constexpr int NA = TT * DA / THREADS, NV = TT * 32 / THREADS;
     T xa[NA], xk[NA], xv[NV];
     auto fetch = [&](int i0) {
         const int m = min(TT, n - i0);
 #pragma unroll
         for (int u = 0; u < NA; ++u) {
-            const int e = tid + 256 * u, i = e / DA, a = e - i * DA;
+            const int e = tid + THREADS * u, i = e / DA, a = e - i * DA;
             const long long t = w.rev ? n - 1 - i0 - i : i0 + i;
             const bool on = i < m && a < w.da;
             xa[u] = xk[u] = 0;
@@ -72,7 +75,7 @@ __global__ void __launch_bounds__(256) k_la_recurrent(const LaArgs p, int slices
         }
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
-            const int e = tid + 256 * u, i = e >> 5, c = c0 + (e & 31);
+            const int e = tid + THREADS * u, i = e >> 5, c = c0 + (e & 31);
             const long long t = w.rev ? n - 1 - i0 - i : i0 + i;
             xv[u] = 0;
             if (i < m && c < w.dc) xv[u] = pv[t * w.sv[1] + c];
@@ -114,29 +117,29 @@ __global__ void __launch_bounds__(256) k_la_recurrent(const LaArgs p, int slices
         // every warp is past the tile before (the barrier in front of its sums)
 #pragma unroll
         for (int u = 0; u < NA; ++u) {
-            const int e = tid + 256 * u;
+            const int e = tid + THREADS * u;
             (&sa[0][0])[e] = R::f(xa[u]);
             (&sk[0][0])[e] = R::f(xk[u]);
         }
 #pragma unroll
-        for (int u = 0; u < NV; ++u) (&sv[0][0])[tid + 256 * u] = R::f(xv[u]) * w.write;
+        for (int u = 0; u < NV; ++u) (&sv[0][0])[tid + THREADS * u] = R::f(xv[u]) * w.write;
         __syncthreads();
         if (i0 + TT < n) fetch(i0 + TT);
         if (w.rev) {
-#pragma unroll 4
+#pragma unroll(NR == 4 ? 8 : 4)
             for (int i = 0; i < m; ++i) token(i, std::true_type{});
         } else {
-#pragma unroll 4
+#pragma unroll(NR == 4 ? 8 : 4)
             for (int i = 0; i < m; ++i) token(i, std::false_type{});
         }
         __syncthreads();
         if (w.o)
-            for (int e = tid; e < m * 32; e += 256) {
+            for (int e = tid; e < m * 32; e += THREADS) {
                 const int i = e >> 5, c = e & 31;
                 if (c0 + c >= w.dc) continue;
                 float o = part[i][0][c];
 #pragma unroll
-                for (int q = 1; q < 8; ++q) o += part[i][q][c];
+                for (int q = 1; q < W; ++q) o += part[i][q][c];
                 const long long t = w.rev ? n - 1 - i0 - i : i0 + i;
                 st_io(w.o, bo + t * w.so[1] + c0 + c, o * w.read, BF16 && !w.o_f32);
             }
@@ -213,7 +216,8 @@ struct StepArgs {
 
 // One token: bound by reading and writing the state.  A block takes 32 columns of a head's
 // state, 16 rows at a time, eight lanes a row with four columns each (VEC), or a lane a
-// column; the partial products with q are added over the rows at the end.
+// column; the partial products with q are added over the rows at the end.  64 rows of 16 heads of
+// 128 x 128 (137 MB there and back): 25.8 us on one B200, 5.2 TB/s, the launch among it.
 template <bool VEC>
 __global__ void __launch_bounds__(128) k_la_step(const StepArgs p, int slices) {
     __shared__ float sq[LA_MAX_DIM], sk[LA_MAX_DIM], red[4][32];
@@ -293,9 +297,10 @@ cudaError_t la_recurrent(const LaArgs &p, cudaStream_t st) {
     }
     const int slices = (dc + 31) / 32;
     const dim3 grid((unsigned)((long long)p.B * p.H * slices), p.nwalk);
-    auto go = [&](auto kern) { kern<<<grid, 256, 0, st>>>(p, slices); };
-    if (da <= 32) p.bf16 ? go(k_la_recurrent<4, 16, true>) : go(k_la_recurrent<4, 16, false>);
-    else if (da <= 64) p.bf16 ? go(k_la_recurrent<8, 16, true>) : go(k_la_recurrent<8, 16, false>);
+    auto go = [&](auto kern, int threads = 256) { kern<<<grid, threads, 0, st>>>(p, slices); };
+    if (da <= 16) p.bf16 ? go(k_la_recurrent<4, 32, true, 4>, 128) : go(k_la_recurrent<4, 32, false, 4>, 128);
+    else if (da <= 32) p.bf16 ? go(k_la_recurrent<4, 32, true>) : go(k_la_recurrent<4, 32, false>);
+    else if (da <= 64) p.bf16 ? go(k_la_recurrent<8, 24, true>) : go(k_la_recurrent<8, 24, false>);
     else if (da <= 128) p.bf16 ? go(k_la_recurrent<16, 16, true>) : go(k_la_recurrent<16, 16, false>);
     else p.bf16 ? go(k_la_recurrent<32, 8, true>) : go(k_la_recurrent<32, 8, false>);
     profile_mark(st, "k_la_recurrent");
