@@ -8,6 +8,7 @@ and SSD-MIMO rank-R routing, as a C-ABI CUDA library (``include/ssm_scan.h``).
 Modules:
   ``abi``        ctypes binding with the C entry-point names
   ``scan``       torch device-buffer helpers around the binding
+  ``layer``      the operators around the mixer: RMS norm, rotary positions, linear attention
   ``cp``         sequence sharding: segment scans joined through boundary values
   ``dist``       data-parallel plumbing (parameter-gradient all-reduce)
   ``synthetic``  seeded input generators (no scan arithmetic)

@@ -8,8 +8,11 @@
 // residual stream, which the backward reads.
 //
 // With many rows a team is a warp (rows up to 2048 bf16 values): no barriers, and 8 x 16
-// bytes a lane and tensor in flight; with a block a row instead, 65536 x 2048 with a row scale took 206 us.
-// With few rows, a decoding step's, a block takes a row, for the shortest chain.
+// bytes a lane and tensor in flight.  On one B200, 65536 x 2048 bf16 with a residual: 160 us without
+// codes (1.07 GB, 6.7 TB/s), 152 with a row scale (0.94 GB, 6.2 TB/s; 206 with a block a
+// row), 178 with block scales, whose maxima go through shuffles; the gradient 232 us
+// (1.07 GB, 4.6 TB/s: the sums of dweight in registers leave a third of the warps).
+// With few rows, a decoding step's, a block takes a row, for the shortest chain (8 x 2048: 2.4 us).
 #include <cuda_fp8.h>
 #include <float.h>
 
