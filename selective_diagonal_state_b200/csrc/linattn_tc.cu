@@ -26,8 +26,10 @@
 //
 // On one B200, 4 x 16384 tokens of 16 heads of 128 / 128: 319 us, 1.08 GB (3.4 TB/s) and 0.5
 // PFLOP/s; 4 x 4096 tokens of 16 heads over 4: 87 us, the gradient 312; 1 x 257: 14 us.  What bounds
-// it is none of the units (tensor pipe 26 %, issue 47 %, HBM 26 %) but the chain of a chunk's
-// steps: scores, P, P V, output, each handed on through a barrier, 2.5 us a chunk.  Steps that
+// it is none of the units (tensor pipe 26 %, issue 47 %, HBM 26 %) but the steps of a chunk handed on
+// from role to role, 2.5 us a chunk: scores, P, P V, output, and K^T V', state, A S.  Taking the
+// output off the first of these chains (P a chunk ahead of it, two accumulators) was no faster, 328 us.
+// Steps that
 // counted: the roles' own warps (a block of 20 warps with all of a chunk's MMAs in one took 351 us);
 // v from L2 by registers instead of out of the V tile (403 to 351); two warps for the MMAs (327).
 // Every role runs its own code once a chunk, so the walk is compiled for each direction and kind of
