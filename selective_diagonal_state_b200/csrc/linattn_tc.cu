@@ -29,8 +29,8 @@
 // it is none of the units (tensor pipe 26 %, issue 47 %, HBM 26 %) but the steps of a chunk handed on
 // from role to role, 2.5 us a chunk: scores, P, P V, output, and K^T V', state, A S.  Taking the
 // output off the first of these chains (P a chunk ahead of it, two accumulators) was no faster, 328 us.
-// Steps that
-// counted: the roles' own warps (a block of 20 warps with all of a chunk's MMAs in one took 351 us);
+// Steps that counted:
+// the roles' own warps (a block of 20 warps with all of a chunk's MMAs in one took 351 us);
 // v from L2 by registers instead of out of the V tile (403 to 351); two warps for the MMAs (327).
 // Every role runs its own code once a chunk, so the walk is compiled for each direction and kind of
 // output and its loops stay rolled: instruction fetch was what bound a kernel of the same
@@ -63,7 +63,7 @@ constexpr int F_UP = F_W + 160;          // [32] lam^u
 constexpr int F_DOWN = F_UP + 32;        // [32] lam^{31 - u}
 constexpr int F_END = F_DOWN + 32;
 constexpr uint32_t SM_BAR = SM_F32 + F_END * 4;
-constexpr uint32_t SMEM_BYTES = SM_BAR + 224 + 1024;
+constexpr uint32_t SMEM_BYTES = SM_BAR + 256 + 1024;
 static_assert(F_UP % 4 == 0 && F_DOWN % 4 == 0, "16-byte rows");
 static_assert(SM_BAR % 8 == 0 && SMEM_BYTES <= 232448, "one block an SM");
 // tensor memory columns
@@ -219,19 +219,21 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return r;
 }
 __device__ __forceinline__ float2 asf2(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
+// Every barrier is waited for before what completes it again can begin (it needs an
+// arrival, or a tile's place, that its waiter gives afterwards), so no completion is missed.
 struct Bars {
     uint64_t a_full[2], k_full[2], v_full[2];   // tiles loaded
     uint64_t a_free[2], k_free[2], v_free[2];   // tiles read by their last product
     uint64_t sc, kv[2], as, o;                  // products done: scores; K^T V' (halves of the tokens); A S; P V
     uint64_t p, vp[2], s;                       // operands written: P, V' (halves), S
     uint64_t kv_read, o_read;                   // results fetched from tensor memory
-    uint64_t o_tile;                            // the output in shared memory, or stored
+    uint64_t o_tile[2];                         // the output in shared memory, or stored
     uint64_t fixed;                             // rows of other tokens are zeros (one chunk of a walk at most)
     uint64_t end[2];
     uint32_t tslot;
     int failed;
 };
-static_assert(sizeof(Bars) <= 224, "barrier space");
+static_assert(sizeof(Bars) <= 256, "barrier space");
 
 // Bounded wait for the completion number `n` (from 0) of a barrier; false when it does not
 // come, and every role that waits for one that has given up gives up too, the block's error
@@ -445,7 +447,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
 #pragma unroll 1
             for (; c < nch; ++c) {
                 const int t0 = chunk(c);
-                if (!await(&B->o_tile, (uint32_t)c)) break;
+                if (!await(&B->o_tile[c & 1], (uint32_t)c >> 1)) break;
                 // what is past L or the head is not written
                 if (OUT == 1) {   // (rows behind the sequence hold nothing that is read)
                     const unsigned char *at = sm + (c & 1) * STAGE + ST_A;
@@ -558,7 +560,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             fence_before_sync();
             warp_arrive(&B->o_read);
             fence_proxy_async();
-            warp_arrive(&B->o_tile);
+            warp_arrive(&B->o_tile[c & 1]);
         }
         over(c >= nch);
     } else if (warp >= 20) {
@@ -774,7 +776,7 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
                 mbar_init(q, q == &B->k_free[i] && !STATE ? 2 : 1);   // K has two readers
         for (uint64_t *q : {&B->sc, &B->kv[0], &B->kv[1], &B->as, &B->o, &B->end[0], &B->end[1]}) mbar_init(q, 1);
         // an arrival a warp
-        for (uint64_t *q : {&B->vp[0], &B->vp[1], &B->s, &B->kv_read, &B->fixed, &B->p, &B->o_read, &B->o_tile}) mbar_init(q, 8);
+        for (uint64_t *q : {&B->vp[0], &B->vp[1], &B->s, &B->kv_read, &B->fixed, &B->p, &B->o_read, &B->o_tile[0], &B->o_tile[1]}) mbar_init(q, 8);
         B->failed = 0;
         mbar_fence_init();
     }
