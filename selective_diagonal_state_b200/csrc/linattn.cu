@@ -273,10 +273,19 @@ __global__ void __launch_bounds__(128) k_la_step(const StepArgs p, int slices) {
         float o = 0.f;
         if (c < p.dv) {
             const float v = ld_io(p.v, vb + c, p.bf16);
-            for (int a = warp; a < p.dk; a += 4) {
-                const float x = fmaf(lam, S[(long long)a * p.dv + c], sk[a] * v);
-                o = fmaf(sq[a], x, o);
-                S[(long long)a * p.dv + c] = x;
+            for (int a0 = warp; a0 < p.dk; a0 += 64) {   // 16 rows on their way at once
+                float x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (a0 + 4 * i < p.dk) x[i] = S[(long long)(a0 + 4 * i) * p.dv + c];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int a = a0 + 4 * i;
+                    if (a >= p.dk) break;
+                    x[i] = fmaf(lam, x[i], sk[a] * v);
+                    o = fmaf(sq[a], x[i], o);
+                    S[(long long)a * p.dv + c] = x[i];
+                }
             }
         }
         red[warp][lane] = o;
