@@ -219,8 +219,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return r;
 }
 __device__ __forceinline__ float2 asf2(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
-// Every barrier is waited for before what completes it again can begin (it needs an
-// arrival, or a tile's place, that its waiter gives afterwards), so no completion is missed.
+// A wait tests a barrier's parity, so it is right only if the completion before the one waited
+// for has happened (else it passes too early) and the one after it cannot happen yet (else it is
+// missed).  The first holds because a role waits for every completion of a barrier in turn, or
+// has waited for what needs the earlier one (a tile's place is free once its products have read
+// it); the second because what completes a barrier again needs an arrival, or a tile's place, that
+// the waiter gives afterwards.  The V' warps do not follow a, v and the scores from chunk to
+// chunk, so for the one chunk whose tiles they touch they have a barrier of its own, `taken`.
 struct Bars {
     uint64_t a_full[2], k_full[2], v_full[2];   // tiles loaded
     uint64_t a_free[2], k_free[2], v_free[2];   // tiles read by their last product
@@ -228,7 +233,8 @@ struct Bars {
     uint64_t p, vp[2], s;                       // operands written: P, V' (halves), S
     uint64_t kv_read, o_read;                   // results fetched from tensor memory
     uint64_t o_tile[2];                         // the output in shared memory, or stored
-    uint64_t fixed;                             // rows of other tokens are zeros (one chunk of a walk at most)
+    uint64_t taken, fixed;                      // one chunk of a walk at most: its tiles have come and its scores have
+                                                // read them; its rows of other tokens are zeros
     uint64_t end[2];
     uint32_t tslot;
     int failed;
@@ -415,7 +421,10 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                         mma_commit(&B->as);
                         if (OUT == 0) mma_commit(&B->a_free[c & 1]);   // else warp 2, when the output has left the tile
                         if (!await(&B->v_full[c & 1], (uint32_t)c >> 1) || !await(&B->p, (uint32_t)c)) break;
-                        if (dirty(c) && !await(&B->fixed, 0u)) break;
+                        if (dirty(c)) {   // P is there, so the scores are done
+                            mbar_arrive(&B->taken);
+                            if (!await(&B->fixed, 0u)) break;
+                        }
                         fence_after_sync();
 #pragma unroll 1
                         for (int q = 0; q < 2; ++q)
@@ -594,10 +603,12 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             unsigned char *st = sm + (c & 1) * STAGE;
             const int n = ntok(c);
             const bool fix = dirty(c);
-            if (__builtin_expect(fix, 0)) {   // the scores have read K
+            if (__builtin_expect(fix, 0)) {
+                // behind `taken` the tiles are the chunk's and stay so until they are fixed; a walk of
+                // the state alone has waited for K^T V' of two chunks ago, the last reader of K's place
+                if (!STATE && !await_warp(&B->taken, 0u)) break;
                 if (!await_warp(&B->k_full[c & 1], (uint32_t)c >> 1)) break;
                 if (!STATE && !await_warp(&B->v_full[c & 1], (uint32_t)c >> 1)) break;
-                if (!STATE && !await_warp(&B->sc, (uint32_t)c)) break;
             }
             if (c > 0 && !await_warp(&B->kv[z], (uint32_t)c - 1u)) break;   // this half has been read
 #pragma unroll 1
@@ -774,7 +785,7 @@ k_la_walk(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
         for (int i = 0; i < 2; ++i)
             for (uint64_t *q : {&B->a_full[i], &B->k_full[i], &B->v_full[i], &B->a_free[i], &B->k_free[i], &B->v_free[i]})
                 mbar_init(q, q == &B->k_free[i] && !STATE ? 2 : 1);   // K has two readers
-        for (uint64_t *q : {&B->sc, &B->kv[0], &B->kv[1], &B->as, &B->o, &B->end[0], &B->end[1]}) mbar_init(q, 1);
+        for (uint64_t *q : {&B->sc, &B->kv[0], &B->kv[1], &B->as, &B->o, &B->taken, &B->end[0], &B->end[1]}) mbar_init(q, 1);
         // an arrival a warp
         for (uint64_t *q : {&B->vp[0], &B->vp[1], &B->s, &B->kv_read, &B->fixed, &B->p, &B->o_read, &B->o_tile[0], &B->o_tile[1]}) mbar_init(q, 8);
         B->failed = 0;

@@ -1,0 +1,82 @@
+"""Which kernel a linear attention call takes, and the walk's paths that depend on where the
+sequences of a padded batch end.  Values against the 64-bit forms with the bounds of
+test_layer_gpu.py."""
+import numpy as np
+import pytest
+
+from selective_diagonal_state_b200 import abi
+from tests.test_layer_gpu import DT, la_case, la_check
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from selective_diagonal_state_b200 import build
+    build.build()
+    abi.load_library()
+
+
+@pytest.fixture(scope="module")
+def layer():
+    from selective_diagonal_state_b200 import layer
+    return layer
+
+
+@pytest.fixture(autouse=True)
+def _no_wait_gave_up():
+    """A bounded wait that gives up is reported behind the call only."""
+    yield
+    abi.ssm_scan_poll_device_error()
+
+
+def kernels(call):
+    """{kernel: launches} of the calls that `call` makes."""
+    abi.ssm_scan_profile_start(64)
+    try:
+        call()
+    finally:
+        got = abi.ssm_scan_profile_stop()
+    return {name: n for name, (n, _) in got.items()}
+
+
+def ragged_case(seed, lengths, L, H, G, dk, dv):
+    """la_case with these lengths, NaN behind them."""
+    T, N = la_case(seed, "bf16", len(lengths), L, H, G, dk, dv, False)
+    N["lengths"] = np.array(lengths)
+    T["lengths"] = torch.from_numpy(N["lengths"].astype(np.int32)).cuda()
+    for name in ("q", "k", "v", "do"):
+        for b, n in enumerate(lengths):
+            T[name][b, n:] = float("nan")
+    return T, N
+
+
+# the chunk that a sequence ends in is the walk's first (reverse) or its last (forward): the third
+# and later ones, whose tiles lie where those of earlier chunks were, at both places
+ENDS = [(257, 390, 513, 639, 640, 700), (383, 384, 385, 511, 0, 899), (255, 256, 129, 1, 768, 300)]
+
+
+@pytest.mark.parametrize("lengths", ENDS)
+@pytest.mark.parametrize("H,G,dk,dv", [(2, 1, 128, 64), (3, 3, 16, 24), (2, 2, 64, 128)])
+def test_sequences_that_end_in_any_chunk(layer, lengths, H, G, dk, dv):
+    L = max(lengths) + (1 if 700 in lengths else 70)
+    T, N = ragged_case(L + dk, lengths, L, H, G, dk, dv)
+    la_check(layer, T, N, "bf16", dk ** -0.5, True)
+    args = [T[x] for x in ("q", "k", "v", "log_decay")]
+    # one walk for each head, not cut into segments
+    assert kernels(lambda: layer.linattn(*args, lengths=T["lengths"])) == {"k_la_walk": 1}
+    back = kernels(lambda: layer.linattn_backward(*args, T["do"], lengths=T["lengths"]))
+    assert back == {"k_la_walk": 1} | ({"k_la_group_sum16": 2} if H > G else {})
+
+
+def test_padded_batch_with_more_walks_than_fit_at_once(layer):
+    """24 heads of 4 rows, the lengths in every chunk of the walk, repeated: always the same bits."""
+    T, N = ragged_case(5, (257, 390, 513, 639), 700, 24, 24, 16, 24)
+    la_check(layer, T, N, "bf16", 0.25, True)
+    args = [T[x] for x in ("q", "k", "v", "log_decay")]
+    first = layer.linattn(*args, state=T["state"], lengths=T["lengths"], out=torch.zeros(4, 700, 24, 24, dtype=DT["bf16"], device="cuda"))
+    for _ in range(20):
+        again = layer.linattn(*args, state=T["state"], lengths=T["lengths"], out=torch.zeros_like(first[0]))
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
