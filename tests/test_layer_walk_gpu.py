@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 
 from selective_diagonal_state_b200 import abi
-from tests.test_layer_gpu import DT, la_case, la_check
+from tests import layer_ref as R
+from tests.test_layer_gpu import DT, close, la_case, la_check
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +81,46 @@ def test_padded_batch_with_more_walks_than_fit_at_once(layer):
     for _ in range(20):
         again = layer.linattn(*args, state=T["state"], lengths=T["lengths"], out=torch.zeros_like(first[0]))
         assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("L,dk,dv", [(33, 64, 64), (17, 128, 128), (17, 64, 128), (257, 8, 8)])
+def test_shortest_sequences_of_the_walk(layer, L, dk, dv):
+    """More than 2048 / head dim tokens take the walk, one less the recurrence."""
+    for n, name, tensor in ((L, "k_la_walk", True), (L - 1, "k_la_recurrent", False)):
+        T, N = la_case(n, "bf16", 2, n, 2, 1, dk, dv, False)
+        la_check(layer, T, N, "bf16", dk ** -0.5, tensor)
+        args = [T[x] for x in ("q", "k", "v", "log_decay")]
+        assert kernels(lambda: layer.linattn(*args)) == {name: 1}
+        assert name in kernels(lambda: layer.linattn_backward(*args, T["do"]))
+
+
+@pytest.mark.parametrize("L,lengths", [(300, None), (400, (129, 390)), (2600, (1279, 2600))])
+def test_values_wider_than_the_keys_may_be(layer, L, lengths):
+    """dim_v above 128, three and four slices: the output and the state on tensor cores, the gradient by
+    the recurrence (a walk of it would have dim_v state rows)."""
+    for dv in (136, 200, 256):
+        T, N = ragged_case(dv, lengths, L, 2, 1, 64, dv) if lengths else la_case(dv, "bf16", 2, L, 2, 1, 64, dv, False)
+        n = N["lengths"]
+        live = np.ones((2, L), bool) if n is None else np.arange(L)[None] < n[:, None]
+        out = torch.zeros(2, L, 2, dv, dtype=DT["bf16"], device="cuda")
+        o, S = layer.linattn(T["q"], T["k"], T["v"], T["log_decay"], state=T["state"], lengths=T["lengths"], out=out)
+        A = {x: np.abs(N[x]) for x in ("q", "k", "v", "state")}
+        ro, rS = R.linattn(N["q"], N["k"], N["v"], N["log_decay"], 0.125, N["state"], n)
+        ob, sb = R.linattn(A["q"], A["k"], A["v"], N["log_decay"], 0.125, A["state"], n)
+        c = (60 * -(-L // 128) + 2 * dv + 16) * R.U32        # as in la_check
+        close("o", o, ro, (R.HALF["bf16"] * np.abs(ro) + (R.HALF["bf16"] + c) * ob) * live[..., None, None])
+        close("state", S, rS, c * sb)
+        args = [T[x] for x in ("q", "k", "v", "log_decay")]
+        assert "k_la_walk" in kernels(lambda: layer.linattn(*args, lengths=T["lengths"]))
+        assert "k_la_recurrent" in kernels(lambda: layer.linattn_backward(*args, T["do"], lengths=T["lengths"]))
+
+
+def test_which_calls_are_cut_and_which_take_the_recurrence(layer):
+    T, _ = la_case(1, "bf16", 1, 2300, 3, 1, 128, 128, False)
+    args = [T[x] for x in ("q", "k", "v", "log_decay")]
+    cut = {"k_la_walk_state": 1, "k_la_segments": 1, "k_la_walk": 1}
+    assert kernels(lambda: layer.linattn(*args)) == cut
+    assert kernels(lambda: layer.linattn(*args, route=abi.LINATTN_RECURRENT)) == {"k_la_recurrent": 1}
+    for t, dim, off in (("fp32", 64, 0), ("bf16", 20, 0), ("bf16", 136, 0), ("bf16", 64, 1)):
+        x = torch.zeros(1, 300, 2, dim + off, dtype=DT[t], device="cuda")[..., off:]
+        assert kernels(lambda: layer.linattn(x, x, x, args[3][:2])) == {"k_la_recurrent": 1}
