@@ -10,8 +10,8 @@ allocator on that stream unless given; calls that overlap on the GPU, captured g
 them, must not share one.
 
 What a call checks and derives from its tensors' shapes, strides and types (never from their
-contents or addresses) is kept for the next call with the same ones: the checks alone would
-take longer than the smallest kernels.
+contents or addresses) is kept for the next call with the same ones, once a call has gone
+through: the checks alone would take longer than the smallest kernels.
 """
 from __future__ import annotations
 
@@ -39,7 +39,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 class _Plan:
     """Descriptor, device and sizes of a call, from its tensors' layouts."""
 
-    __slots__ = ("dev", "desc", "lib", "ws", "likes")
+    __slots__ = ("dev", "desc", "lib", "ws", "likes", "key")   # key: None once the plan is kept
 
 
 def _sig(t):
@@ -49,7 +49,10 @@ def _sig(t):
 def _like(shape, dtype, dev):
     """What ``torch.empty_like`` takes for a dense tensor of this shape (one value, expanded:
     a third of the time of ``torch.empty`` with its arguments)."""
-    return torch.empty((), dtype=dtype, device=dev).expand(shape)
+    t = torch.empty((), dtype=dtype, device=dev)
+    if type(t) is not torch.Tensor:     # a mode that makes tensors without memory is on
+        raise ValueError("the tensors of a call must have memory on their device (no fake tensors)")
+    return t.expand(shape)
 
 
 _new = torch.empty_like
@@ -60,10 +63,15 @@ def _plan(key, make, *args):
     if p is None:
         p = make(*args)
         p.lib = abi.load_library()
-        if len(_PLANS) >= _MOST_PLANS:
-            _PLANS.clear()
-        _PLANS[key] = p
+        p.key = key
     return p
+
+
+def _keep(p):
+    if len(_PLANS) >= _MOST_PLANS:
+        _PLANS.clear()
+    key, p.key = p.key, None
+    _PLANS[key] = p
 
 
 def _device(first, *tensors):
@@ -94,9 +102,13 @@ def _elsewhere(dev, stream):
 def _on_device(go, p, stream, *args):
     """go(plan, raw stream, ...) on the plan's device and the caller's stream."""
     if stream is None and _current_device() == p.dev:
-        return go(p, _raw_stream(p.dev), *args)
-    with _elsewhere(p.dev, stream) as st:
-        return go(p, st, *args)
+        out = go(p, _raw_stream(p.dev), *args)
+    else:
+        with _elsewhere(p.dev, stream) as st:
+            out = go(p, st, *args)
+    if p.key is not None:
+        _keep(p)
+    return out
 
 
 def _ptr(t):

@@ -263,6 +263,27 @@ def test_host_tensors_refused():
         layer.linattn(q, q, q, torch.zeros(2))
 
 
+def test_tensors_without_memory_are_refused_and_leave_nothing_behind():
+    """A call under a mode that makes fake tensors keeps no plan: a later call of the same layout
+    would take its outputs from fake prototypes."""
+    torch = pytest.importorskip("torch")
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    from selective_diagonal_state_b200 import layer
+    before = dict(layer._PLANS)
+    with FakeTensorMode():
+        x = torch.empty(4, 256, dtype=torch.bfloat16, device="cuda")
+        q, dec = torch.empty(1, 3, 2, 8, device="cuda"), torch.empty(2, device="cuda")
+        freq, state = torch.empty(4, dtype=torch.float64, device="cuda"), torch.empty(1, 2, 8, 8, device="cuda")
+        for call in (lambda: layer.rmsnorm(x), lambda: layer.rmsnorm(x[:0], quant="row"),
+                     lambda: layer.rmsnorm_backward(x, x, None, x[:, 0].float()), lambda: layer.rope(q, q, freq),
+                     lambda: layer.linattn(q, q, q, dec), lambda: layer.linattn_backward(q, q, q, dec, q),
+                     lambda: layer.linattn_step(q[:, :1], q[:, :1], q[:, :1], dec, state)):
+            with pytest.raises(ValueError, match="memory"):
+                call()
+    assert layer._PLANS == before
+
+
 def test_reference_gradients_against_differences():
     """The 64-bit gradients the kernels are held to, against central differences."""
     g = np.random.default_rng(0)

@@ -492,6 +492,29 @@ def test_numbers_given_as_tensors_are_read_every_call(layer):
     assert not torch.equal(layer.rmsnorm(q, eps=e).y, n)
 
 
+def test_calls_under_a_fake_mode_leave_the_next_ones_alone(layer):
+    """Before and after a real call of the same layout: refused, and the real one gives the same."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    g = np.random.default_rng(6)
+    x, _ = draw(g, (3, 88), "bf16")
+    w = torch.ones(88, device="cuda")
+    want = None
+    for _ in range(2):
+        with FakeTensorMode():
+            y, v = torch.empty(3, 88, dtype=torch.bfloat16, device="cuda"), torch.empty(88, device="cuda")
+            for r in (None, y):
+                with pytest.raises(Exception):
+                    layer.rmsnorm(y, v, r=r, want_rstd=True)
+            with pytest.raises(Exception):
+                layer.rmsnorm(y[:0], v, want_rstd=True)
+        f = layer.rmsnorm(x, w, want_rstd=True)
+        e = layer.rmsnorm(x[:0], w, want_rstd=True)
+        assert type(f.y) is type(f.rstd) is type(e.y) is torch.Tensor and f.y.data_ptr() and f.rstd.data_ptr()
+        if want is not None:
+            assert torch.equal(f.y, want.y) and torch.equal(f.rstd, want.rstd)
+        want = f
+
+
 def test_helpers_refuse(layer):
     q = torch.zeros(2, 200, 4, 64, dtype=torch.bfloat16, device="cuda")
     dec = torch.zeros(4, device="cuda")
