@@ -49,10 +49,10 @@ def _sig(t):
 def _like(shape, dtype, dev):
     """What ``torch.empty_like`` takes for a dense tensor of this shape (one value, expanded:
     a third of the time of ``torch.empty`` with its arguments)."""
-    t = torch.empty((), dtype=dtype, device=dev)
+    t = torch.empty((0,) if 0 in shape else (), dtype=dtype, device=dev)
     if type(t) is not torch.Tensor:     # a mode that makes tensors without memory is on
         raise ValueError("the tensors of a call must have memory on their device (no fake tensors)")
-    return t.expand(shape)
+    return t.view(shape) if 0 in shape else t.expand(shape)    # (of nothing, the strides would stay 0)
 
 
 _new = torch.empty_like
@@ -171,6 +171,8 @@ class Normed:
 
 def _rows(t, name, dim):
     """Row stride of [..., dim] seen as evenly spaced rows."""
+    if t.numel() == 0:
+        return dim
     step = n = None
     for size, stride in zip(t.shape[-2::-1], t.stride()[-2::-1]):
         if size == 1:

@@ -263,6 +263,22 @@ def test_host_tensors_refused():
         layer.linattn(q, q, q, torch.zeros(2))
 
 
+def test_row_strides():
+    """Of evenly spaced rows, of which there may be none whatever the leading dimensions."""
+    torch = pytest.importorskip("torch")
+    from selective_diagonal_state_b200 import layer
+    for shape, step in (((5, 8), 8), ((2, 3, 8), 8), ((2, 0, 8), 8), ((0, 3, 8), 8), ((2, 3, 0, 8), 8), ((8,), 8), ((1, 1, 8), 8)):
+        assert layer._rows(torch.empty(shape), "x", 8) == step
+    assert layer._rows(torch.empty(4, 3, 16)[..., :8], "x", 8) == 16
+    assert layer._rows(torch.empty(4, 3, 8)[:, 1], "x", 8) == 24
+    assert layer._rows(torch.empty(1, 8).expand(6, 8), "x", 8) == 0
+    with pytest.raises(ValueError, match="evenly"):
+        layer._rows(torch.empty(4, 3, 8)[:, :2], "x", 8)
+    for shape in ((2, 3, 8), (2, 0, 8), (0, 3), (1, 1, 8), (2, 1, 4, 1)):      # the helpers' outputs are dense
+        out = torch.empty_like(layer._like(shape, torch.float32, "cpu"))
+        assert out.shape == shape and out.stride() == torch.empty(shape).stride()
+
+
 def test_tensors_without_memory_are_refused_and_leave_nothing_behind():
     """A call under a mode that makes fake tensors keeps no plan: a later call of the same layout
     would take its outputs from fake prototypes."""

@@ -175,6 +175,20 @@ def test_norm_in_place_and_broadcast(layer):
     assert dx.shape == (0, 512) and (dw == 0).all()
 
 
+@pytest.mark.parametrize("shape", [(2, 0, 512), (2, 3, 0, 64), (0, 4, 33)])
+def test_norm_of_no_rows(layer, shape):
+    """A batch of empty prompts: empty outputs, no gradient of the weight."""
+    x = torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(shape[-1], device="cuda")
+    f = layer.rmsnorm(x, w, residual=x, want_rstd=True)
+    assert f.y.shape == f.r.shape == shape and f.rstd.shape == shape[:-1]
+    dx, dw = layer.rmsnorm_backward(x, f.r, w, f.rstd, dr=x)
+    assert dx.shape == shape and dw.shape == w.shape and (dw == 0).all()
+    if shape[-1] == 512:
+        c = layer.rmsnorm(x, w, residual=x, quant="block")
+        assert c.y8.shape == shape and c.scales.shape == (*shape[:-1], 4)
+
+
 # ---- rotary positions ------------------------------------------------------------------
 
 @pytest.mark.parametrize("t", ["bf16", "fp32"])
