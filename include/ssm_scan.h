@@ -591,7 +591,7 @@ SSM_API const char *ssm_scan_last_error(void);
 
 /*
  * Synchronise `stream` and report device-side errors raised by bounded waits
- * inside the kernels since the previous poll (SSM_ERR_TIMEOUT), or a sticky
+ * inside the kernels (ssm_linattn_* among them) since the previous poll (SSM_ERR_TIMEOUT), or a sticky
  * CUDA error (SSM_ERR_CUDA).  Clears the device error word.
  */
 SSM_API int ssm_scan_poll_device_error(void *stream);
@@ -616,7 +616,10 @@ SSM_API int ssm_scan_profile_stop(char *names, int name_len, int *counts, double
  * Failure-path diagnostic (the pages have no counterpart).  The chained
  * tensor-core kernels wait, on the device, for the chunk before (forward) or
  * after (backward) to publish its carry; each such wait polls at most this
- * many times (default 2^22, about half a second) before it gives up.  A wait
+ * many times (default 2^22, about half a second) before it gives up.  The walk
+ * of ssm_linattn_* waits for nothing outside its block, but its warps wait for one another: each of
+ * those waits polls at most this many times too, and at most 2^15 times (about half a second, as its
+ * polls sleep).  A wait
  * that gives up stops every kernel of that call early (its outputs are then
  * undefined), and the next ssm_scan_poll_device_error reports SSM_ERR_TIMEOUT;
  * later calls are unaffected.  0 makes every such wait give up at once: tests

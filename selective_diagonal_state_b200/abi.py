@@ -443,8 +443,8 @@ def ssm_scan_poll_device_error(stream=None) -> None:
 
 
 def ssm_scan_set_wait_limit(polls: int) -> int:
-    """Polls of a carry counter before a chained kernel's wait gives up (0: every
-    such wait gives up); returns the previous limit."""
+    """Polls of a carry counter before a chained kernel's wait gives up, and of a wait within a block
+    of the linear attention walk (0: every such wait gives up); returns the previous limit."""
     rc = int(load_library().ssm_scan_set_wait_limit(int(polls)))
     if rc < 0:
         _check(rc, "ssm_scan_set_wait_limit")

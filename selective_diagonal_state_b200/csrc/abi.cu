@@ -456,6 +456,7 @@ int abi_fail(int code, const char *msg) { return fail(code, "%s", msg); }
 void abi_ok() { g_last_error.clear(); }
 void abi_profile_begin(cudaStream_t st) { profile_begin(st); }
 void abi_profile_end() { profile_end(); }
+long long abi_wait_limit() { return g_wait_limit.load(); }
 void profile_mark(cudaStream_t st, const char *name) {
     if (!g_prof.active || g_prof.cur < 0 || g_prof.used >= g_prof.pool.size()) return;
     cudaEventRecord(g_prof.pool[g_prof.used], st);

@@ -11,6 +11,7 @@ namespace ssm {
 
 int sm_count();
 void profile_mark(cudaStream_t st, const char *name);
+long long abi_wait_limit();   // ssm_scan_set_wait_limit's
 
 cudaError_t rmsnorm_forward(const ssm_rmsnorm_desc_t &d, const void *x, const void *residual,
                             const float *weight, void *r, void *y, void *y8, float *scales,

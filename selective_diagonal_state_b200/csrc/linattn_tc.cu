@@ -48,7 +48,6 @@ __device__ int ssm_la_error_word;
 namespace la {
 
 using namespace umma;
-using chunkc::WAIT_LIMIT;
 
 constexpr int C = 128;                   // tokens of a chunk
 constexpr int THREADS = 896;
@@ -82,6 +81,7 @@ struct Args {
     float *seg[3];   // [segment][b H + h][da][dc]: what a segment adds, then its entering state
     int nseg, G;     // segments of G chunks
     int slices;      // 64-column slices, the most of all walks
+    uint32_t polls;  // of a wait of a role for another (await)
 };
 
 // Descriptor (umma.cuh, sdesc) of 128-byte-swizzled rows with leading offset LBO, at an address
@@ -244,11 +244,13 @@ static_assert(sizeof(Bars) <= 256, "barrier space");
 // Bounded wait for the completion number `n` (from 0) of a barrier; false when it does not
 // come, and every role that waits for one that has given up gives up too, the block's error
 // raised at its end.  The hint lets the hardware keep the thread suspended between polls.
+// A role's waits poll as often as the call says (at most POLLS times, ssm_scan_set_wait_limit);
+// those for a warp's own copies and products, at its end, always POLLS times.
 constexpr uint32_t POLL_NS = 20000, POLLS = 1u << 15;   // about half a second
-__device__ __forceinline__ bool await(uint64_t *bar, uint32_t n) {
+__device__ __forceinline__ bool await(uint64_t *bar, uint32_t n, uint32_t polls) {
     const uint32_t a = smem_u32(bar);
 #pragma unroll 1
-    for (uint32_t i = 0; i < POLLS; ++i) {
+    for (uint32_t i = 0; i < polls; ++i) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
@@ -262,8 +264,8 @@ __device__ __forceinline__ bool await(uint64_t *bar, uint32_t n) {
     return false;
 }
 // The same for a whole warp, all lanes alike.
-__device__ __forceinline__ bool await_warp(uint64_t *bar, uint32_t n) {
-    return __all_sync(0xffffffffu, await(bar, n));
+__device__ __forceinline__ bool await_warp(uint64_t *bar, uint32_t n, uint32_t polls) {
+    return __all_sync(0xffffffffu, await(bar, n, polls));
 }
 // One arrival a warp, after all its lanes are done.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
@@ -284,6 +286,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
     float *f32 = reinterpret_cast<float *>(sm + SM_F32);
     Bars *B = reinterpret_cast<Bars *>(sm + SM_BAR);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t polls = A.polls;
     // chunk number c of the walk: its first token and its tokens
     auto chunk = [&](int c) { return C * (first + (REV ? nch - 1 - c : c)); };
     // the chunk that the sequence ends in, if it is a short one, and its tokens
@@ -348,14 +351,14 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                     }
                     tma_prefetch_4d(&maps.v, c0, hv, tn, b);
                 }
-                if (c >= 2 && !await(&B->k_free[c & 1], n)) break;
+                if (c >= 2 && !await(&B->k_free[c & 1], n, polls)) break;
                 load_k(c);
                 ++got_k;
                 if (STATE) continue;
-                if (c >= 2 && !await(&B->a_free[c & 1], n)) break;
+                if (c >= 2 && !await(&B->a_free[c & 1], n, polls)) break;
                 load_a(c);
                 ++got_a;
-                if (c >= 2 && !await(&B->v_free[c & 1], n)) break;
+                if (c >= 2 && !await(&B->v_free[c & 1], n, polls)) break;
                 load_v(c);
                 ++got_v;
             }
@@ -365,7 +368,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             for (uint32_t i = 0; i < 6; ++i) {
                 const uint32_t got = i < 2 ? got_a : i < 4 ? got_k : got_v, back = 1 + (i & 1);
                 uint64_t *full = i < 2 ? B->a_full : i < 4 ? B->k_full : B->v_full;
-                if (got >= back) await(&full[(got - back) & 1], (got - back) >> 1);
+                if (got >= back) await(&full[(got - back) & 1], (got - back) >> 1, POLLS);
             }
         }
         __syncwarp();
@@ -383,12 +386,12 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
 #pragma unroll 1
                 for (; c < nch; ++c) {
                     const uint32_t st = u0 + ((c & 1) ? STAGE >> 4 : 0u);
-                    if (!await(&B->k_full[c & 1], (uint32_t)c >> 1)) break;
-                    if (c > 0 && !await(&B->kv_read, (uint32_t)c - 1u)) break;
+                    if (!await(&B->k_full[c & 1], (uint32_t)c >> 1, polls)) break;
+                    if (c > 0 && !await(&B->kv_read, (uint32_t)c - 1u, polls)) break;
                     int z = 0;
 #pragma unroll 1
                     for (; z < 2; ++z) {
-                        if (!await(&B->vp[z], (uint32_t)c)) break;
+                        if (!await(&B->vp[z], (uint32_t)c, polls)) break;
                         fence_after_sync();
 #pragma unroll
                         for (int s = 0; s < 4; ++s)
@@ -414,16 +417,16 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                 for (c = -1; c < nch; ++c) {
                     const uint32_t st = u0 + ((c & 1) ? STAGE >> 4 : 0u);
                     if (c >= 0) {
-                        if (!await(&B->s, (uint32_t)c)) break;
-                        if (c > 0 && !await(&B->o_read, (uint32_t)c - 1u)) break;
+                        if (!await(&B->s, (uint32_t)c, polls)) break;
+                        if (c > 0 && !await(&B->o_read, (uint32_t)c - 1u, polls)) break;
                         fence_after_sync();
                         over_head(tm + TM_OS, st + (ST_A >> 4), u0 + (SM_S >> 4), id_n, false);
                         mma_commit(&B->as);
                         if (OUT == 0) mma_commit(&B->a_free[c & 1]);   // else warp 2, when the output has left the tile
-                        if (!await(&B->v_full[c & 1], (uint32_t)c >> 1) || !await(&B->p, (uint32_t)c)) break;
+                        if (!await(&B->v_full[c & 1], (uint32_t)c >> 1, polls) || !await(&B->p, (uint32_t)c, polls)) break;
                         if (dirty(c)) {   // P is there, so the scores are done
                             mbar_arrive(&B->taken);
-                            if (!await(&B->fixed, 0u)) break;
+                            if (!await(&B->fixed, 0u, polls)) break;
                         }
                         fence_after_sync();
 #pragma unroll 1
@@ -436,7 +439,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
                     }
                     if (c + 1 < nch) {   // the scores of the next chunk; P's warps have fetched this one's
                         const uint32_t sn = u0 + ((c & 1) ? 0u : STAGE >> 4), n = (uint32_t)(c + 1) >> 1;
-                        if (!await(&B->k_full[(c + 1) & 1], n) || !await(&B->a_full[(c + 1) & 1], n)) break;
+                        if (!await(&B->k_full[(c + 1) & 1], n, polls) || !await(&B->a_full[(c + 1) & 1], n, polls)) break;
                         fence_after_sync();
                         over_head(tm + TM_SC, sn + (ST_A >> 4), sn + (ST_K >> 4), id_sc, true);
                         mma_commit(&B->sc);
@@ -447,7 +450,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             over(c >= nch);
             uint64_t *end = &B->end[warp >> 1];
             mma_commit(end);   // every MMA is over before tensor memory goes
-            await(end, 0u);
+            await(end, 0u, POLLS);
         }
         __syncwarp();
     } else if (!STATE && warp == 2) {
@@ -456,7 +459,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
 #pragma unroll 1
             for (; c < nch; ++c) {
                 const int t0 = chunk(c);
-                if (!await(&B->o_tile[c & 1], (uint32_t)c >> 1)) break;
+                if (!await(&B->o_tile[c & 1], (uint32_t)c >> 1, polls)) break;
                 // what is past L or the head is not written
                 if (OUT == 1) {   // (rows behind the sequence hold nothing that is read)
                     const unsigned char *at = sm + (c & 1) * STAGE + ST_A;
@@ -480,7 +483,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
 #pragma unroll 1
         for (; c < nch; ++c) {
             const int t0 = chunk(c), n = ntok(c);
-            if (!await_warp(&B->sc, (uint32_t)c)) break;
+            if (!await_warp(&B->sc, (uint32_t)c, polls)) break;
             fence_after_sync();
             // P[i][j] = read write lam^{|i - j|} (a_i . k_j) on one side of the diagonal, 32 columns
             // at a time
@@ -530,7 +533,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             tmem_wait_st();
             fence_before_sync();
             warp_arrive(&B->p);
-            if (!await_warp(&B->o, (uint32_t)c)) break;
+            if (!await_warp(&B->o, (uint32_t)c, polls)) break;
             fence_after_sync();
             const float e = w.read * f32[F_PW + max(0, REV ? n - 1 - row : row + 1)];
             const float2 ee = make_float2(e, e);
@@ -606,11 +609,11 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             if (__builtin_expect(fix, 0)) {
                 // behind `taken` the tiles are the chunk's and stay so until they are fixed; a walk of
                 // the state alone has waited for K^T V' of two chunks ago, the last reader of K's place
-                if (!STATE && !await_warp(&B->taken, 0u)) break;
-                if (!await_warp(&B->k_full[c & 1], (uint32_t)c >> 1)) break;
-                if (!STATE && !await_warp(&B->v_full[c & 1], (uint32_t)c >> 1)) break;
+                if (!STATE && !await_warp(&B->taken, 0u, polls)) break;
+                if (!await_warp(&B->k_full[c & 1], (uint32_t)c >> 1, polls)) break;
+                if (!STATE && !await_warp(&B->v_full[c & 1], (uint32_t)c >> 1, polls)) break;
             }
-            if (c > 0 && !await_warp(&B->kv[z], (uint32_t)c - 1u)) break;   // this half has been read
+            if (c > 0 && !await_warp(&B->kv[z], (uint32_t)c - 1u, polls)) break;   // this half has been read
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
                 const int r = (t >> 3) + 64 * z + 32 * i;
@@ -704,7 +707,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
 #pragma unroll 1
         for (; c < nch; ++c) {
             if (!STATE) {   // S in bf16, the layout of a V tile; A S of the chunk before has read it
-                if (c > 0 && !await_warp(&B->as, (uint32_t)c - 1u)) break;
+                if (c > 0 && !await_warp(&B->as, (uint32_t)c - 1u, polls)) break;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint4 v = make_uint4(pack2(S[4 * q].x, S[4 * q].y), pack2(S[4 * q + 1].x, S[4 * q + 1].y),
@@ -717,7 +720,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
             const float E = f32[F_PW + ntok(c)];
             const float2 EE = make_float2(E, E);
             const uint32_t tk = tm + TM_KV + lane_q + 32u * half;
-            if (!await_warp(&B->kv[1], (uint32_t)c)) break;
+            if (!await_warp(&B->kv[1], (uint32_t)c, polls)) break;
             fence_after_sync();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -736,7 +739,7 @@ __device__ __forceinline__ void walk(const Args &A, const Maps &maps, const LaWa
         }
         over(c >= nch);
         if (dst) {
-            if (!STATE && c >= nch && nch > 0) await_warp(&B->as, (uint32_t)nch - 1u);   // A S has read the operand
+            if (!STATE && c >= nch && nch > 0) await_warp(&B->as, (uint32_t)nch - 1u, polls);   // A S has read the operand
             if (stc == 1) {
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
@@ -900,6 +903,8 @@ bool la_chunked(const LaArgs &p, int nseg, float *const *seg, cudaStream_t st, c
     Args A = {};
     A.p = p;
     A.slices = 0;
+    const long long limit = abi_wait_limit();
+    A.polls = limit < POLLS ? (uint32_t)limit : POLLS;
     for (int i = 0; i < p.nwalk; ++i) {
         const LaWalk &w = p.w[i];
         auto ok = [](const void *q, const long long *s, int el) {

@@ -124,3 +124,29 @@ def test_which_calls_are_cut_and_which_take_the_recurrence(layer):
     for t, dim, off in (("fp32", 64, 0), ("bf16", 20, 0), ("bf16", 136, 0), ("bf16", 64, 1)):
         x = torch.zeros(1, 300, 2, dim + off, dtype=DT[t], device="cuda")[..., off:]
         assert kernels(lambda: layer.linattn(x, x, x, args[3][:2])) == {"k_la_recurrent": 1}
+
+
+@pytest.mark.parametrize("B,L,H,G,dk,dv,ragged", [(2, 700, 2, 1, 64, 64, False), (3, 700, 2, 1, 128, 64, True),
+                                                  (1, 2300, 3, 1, 128, 128, False), (2, 40, 2, 2, 64, 64, False)])
+def test_a_wait_that_gives_up_is_reported_and_the_next_call_is_right(layer, B, L, H, G, dk, dv, ragged):
+    """With no polls allowed every wait of a walk's warps for one another gives up where it does not pass at
+    once; the call ends (its copies and products in flight are still waited for), and the poll reports it."""
+    T, _ = la_case(L, "bf16", B, L, H, G, dk, dv, ragged)
+    args = [T[x] for x in ("q", "k", "v", "log_decay")]
+    calls = (lambda: layer.linattn(*args, state=T["state"], lengths=T["lengths"], out=torch.zeros(B, L, H, dv, dtype=DT["bf16"], device="cuda")),
+             lambda: layer.linattn_backward(*args, T["do"], state=T["state"], dstate=T["dstate"], lengths=T["lengths"],
+                                            out=[torch.zeros_like(T[x]) for x in ("q", "k", "v")]))
+    want = [call() for call in calls]
+    abi.ssm_scan_poll_device_error()
+    for call, ref in zip(calls, want):
+        old = abi.ssm_scan_set_wait_limit(0)
+        try:
+            call()
+            with pytest.raises(abi.SsmError) as e:
+                abi.ssm_scan_poll_device_error()
+            assert e.value.code == -5        # SSM_ERR_TIMEOUT
+        finally:
+            abi.ssm_scan_set_wait_limit(old)
+        got = call()
+        abi.ssm_scan_poll_device_error()     # cleared by the poll above, and nothing new
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
