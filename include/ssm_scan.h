@@ -444,7 +444,8 @@ typedef struct ssm_rmsnorm_desc {
  * receives the result in dtype_io.  Otherwise y8 receives e4m3 codes and scales (fp32
  * [rows][1] or [rows][dim / 128], dense) the scale of each row or block:
  *     scale = max|y| / 448,   code = e4m3(y 448 / max|y|)     (y in fp32, not rounded first)
- * so that code * scale approximates y; a block of zeros has codes and scale 0, one that
+ * so that code * scale approximates y.  A block of zeros has codes and scale 0; one whose scale would be
+ * below 2^-127 has 2^-127 and codes to it; one that
  * holds a NaN or an infinity has that scale.  y may then be NULL, or receives the
  * unquantised result too.  rstd (fp32 [rows], may be NULL) is what ssm_rmsnorm_bwd reads.
  */

@@ -14,7 +14,6 @@
 // (1.07 GB, 4.6 TB/s: the sums of dweight in registers leave a third of the warps).
 // With few rows, a decoding step's, a block takes a row, for the shortest chain (8 x 2048: 2.4 us).
 #include <cuda_fp8.h>
-#include <float.h>
 
 #include "common.cuh"
 #include "layer.h"
@@ -66,9 +65,11 @@ __device__ __forceinline__ float top(float a, float b) {
     return m;
 }
 
-__device__ __forceinline__ float code_scale(float amax) {
-    // 448 / amax, finite for the smallest blocks; a block of zeros has codes 0
-    return fminf(E4M3_MAX / amax, FLT_MAX);
+// What codes are values times, 448 / amax, and what values are codes times.  Both stay finite for the
+// smallest blocks, and each other's inverse: 2^127 and 2^-127 there.  A block of zeros has codes and scale 0.
+__device__ __forceinline__ float code_scale(float amax) { return fminf(E4M3_MAX / amax, 0x1p127f); }
+__device__ __forceinline__ float value_scale(float amax) {
+    return top(amax / E4M3_MAX, amax > 0.f ? 0x1p-127f : 0.f);
 }
 __device__ __forceinline__ uint16_t e4m3x2(float a, float b) {
     return (uint16_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) k_rmsnorm_fwd(const FwdArgs
     }
     if (QUANT == SSM_QUANT_ROW) {
         whole = team_reduce<T, true>(whole, buf);
-        if (live && lane == 0) p.scales[row] = whole / E4M3_MAX;
+        if (live && lane == 0) p.scales[row] = value_scale(whole);
     }
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) k_rmsnorm_fwd(const FwdArgs
 #pragma unroll
             for (int o = 64 / N; o > 0; o >>= 1) m = top(m, __shfl_xor_sync(0xffffffffu, m, o));
             if (live && v < nv && v % (128 / N) == 0)
-                p.scales[row * (p.dim / 128) + v / (128 / N)] = m / E4M3_MAX;
+                p.scales[row * (p.dim / 128) + v / (128 / N)] = value_scale(m);
         }
         const float c = code_scale(m);
         if (live && v < nv) {
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(256) k_rmsnorm_fwd_any(const FwdArgs p) {
     if (p.quant == SSM_QUANT_ROW) {
         for (int i = threadIdx.x; i < p.dim; i += 256) whole = top(whole, fabsf(value(i)));
         whole = team_reduce<256, true>(whole, buf);
-        if (threadIdx.x == 0) p.scales[row] = whole / E4M3_MAX;
+        if (threadIdx.x == 0) p.scales[row] = value_scale(whole);
     }
     if (p.quant == SSM_QUANT_BLOCK) {   // a warp a block
         for (int b = threadIdx.x / 32; b < p.dim / 128; b += 8) {
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(256) k_rmsnorm_fwd_any(const FwdArgs p) {
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = top(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if ((threadIdx.x & 31) == 0) p.scales[row * (p.dim / 128) + b] = m / E4M3_MAX;
+            if ((threadIdx.x & 31) == 0) p.scales[row * (p.dim / 128) + b] = value_scale(m);
             const float c = code_scale(m);
 #pragma unroll
             for (int j = 0; j < 4; ++j)

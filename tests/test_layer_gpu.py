@@ -151,6 +151,29 @@ def test_norm_codes_of_zeros_tiny_and_broken_rows(layer):
         assert not torch.isfinite(f.scales[3]).all() and not torch.isfinite((code[2] * 1.0)).all()
 
 
+@pytest.mark.parametrize("quant", ["row", "block"])
+@pytest.mark.parametrize("dim,off", [(256, 0), (256, 1), (20480, 0)])
+def test_norm_codes_of_values_near_the_smallest(layer, quant, dim, off):
+    """448 / max|y| is not finite in fp32 below 1.4e-36: a scale is then 2^-127, and codes times scales are still the
+    values, down to subnormals."""
+    g = np.random.default_rng(dim + off)
+    tops = 10.0 ** -np.arange(30.0, 43.0)
+    y = g.uniform(-1, 1, (len(tops), dim + 2 * off)) * tops[:, None]
+    y[:, off::128] = tops[:, None]                  # a largest value in each block
+    x = torch.from_numpy(y.astype(np.float32)).cuda()[:, off: off + dim]
+    xn = np64(x)
+    f = layer.rmsnorm(x, eps=1.0, quant=quant)      # rstd is 1: y = x
+    width = 128 if quant == "block" else dim
+    top = np.abs(xn).reshape(len(tops), -1, width).max(-1)
+    scale = np.maximum(top / 448, 2.0 ** -127)
+    want = xn / np.repeat(scale, width, 1)
+    code = f.y8.float().double().cpu().numpy()
+    # fp32's subnormals are exact inputs here; a division, a product, then half a step of e4m3
+    assert (np.abs(code - want) <= np.maximum(R.HALF["e4m3"] * np.abs(want), 2.0 ** -10) + 8 * R.U32 * np.abs(want)).all()
+    # a scale is rounded to fp32's numbers, subnormal ones among them (steps of 2^-149)
+    assert (np.abs(np64(f.scales) - scale) <= 2 * R.U32 * scale + 2.0 ** -149).all()
+
+
 def test_norm_in_place_and_broadcast(layer):
     """The sum may overwrite x or the residual; a residual may be one row for all."""
     g = np.random.default_rng(8)
