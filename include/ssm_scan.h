@@ -445,8 +445,9 @@ typedef struct ssm_rmsnorm_desc {
  * [rows][1] or [rows][dim / 128], dense) the scale of each row or block:
  *     scale = max|y| / 448,   code = e4m3(y 448 / max|y|)     (y in fp32, not rounded first)
  * so that code * scale approximates y.  A block of zeros has codes and scale 0; one whose scale would be
- * below 2^-127 has 2^-127 and codes to it; one that
- * holds a NaN or an infinity has that scale.  y may then be NULL, or receives the
+ * below 2^-127 has 2^-127 and codes to it; one whose y holds a NaN has scale NaN.  (An infinity in
+ * r makes the row's rstd 0, its y NaN in that place and 0 in the others: a block scale of the row
+ * without such a place is 0.)  y may then be NULL, or receives the
  * unquantised result too.  rstd (fp32 [rows], may be NULL) is what ssm_rmsnorm_bwd reads.
  */
 SSM_API int ssm_rmsnorm_fwd(const ssm_rmsnorm_desc_t *d, const void *x, const void *residual,

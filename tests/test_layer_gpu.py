@@ -151,6 +151,24 @@ def test_norm_codes_of_zeros_tiny_and_broken_rows(layer):
         assert not torch.isfinite(f.scales[3]).all() and not torch.isfinite((code[2] * 1.0)).all()
 
 
+@pytest.mark.parametrize("dim,off", [(256, 0), (256, 1), (20480, 0)])
+def test_norm_codes_of_a_row_with_an_infinity(layer, dim, off):
+    """The infinity makes rstd 0: NaN in its place, 0 in the others, and scales of what is there."""
+    x = torch.ones(3, dim + 2 * off, device="cuda")[:, off: off + dim]
+    x[1, 130] = float("inf")
+    f = layer.rmsnorm(x, quant="row", want_y=True)
+    b = layer.rmsnorm(x, quant="block", want_y=True)
+    for c in (f, b):
+        code = c.y8.float()
+        assert torch.isnan(c.y[1, 130]) and torch.isnan(code[1, 130])
+        assert (c.y[1, :130] == 0).all() and (c.y[1, 131:] == 0).all()
+        for row in (0, 2):
+            assert torch.isfinite(c.scales[row]).all() and (code[row] == 448).all()
+    assert torch.isnan(f.scales[1]).all()
+    assert torch.isnan(b.scales[1, 1]) and (b.scales[1, 0] == 0) and (b.scales[1, 2:] == 0).all()
+    assert (b.y8.float()[1, :128] == 0).all() and (b.y8.float()[1, 256:] == 0).all()
+
+
 @pytest.mark.parametrize("quant", ["row", "block"])
 @pytest.mark.parametrize("dim,off", [(256, 0), (256, 1), (20480, 0)])
 def test_norm_codes_of_values_near_the_smallest(layer, quant, dim, off):
@@ -196,6 +214,34 @@ def test_norm_in_place_and_broadcast(layer):
     e = layer.rmsnorm(x[:0], w, want_rstd=True)
     dx, dw = layer.rmsnorm_backward(dy[:0], x[:0], w, e.rstd)
     assert dx.shape == (0, 512) and (dw == 0).all()
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("quant", ["row", "block"])
+@pytest.mark.parametrize("rows,dim,off", [(3, 2048, 0), (4, 384, 1), (2, 20480, 0), (700, 512, 0)])
+def test_norm_codes_behind_a_residual(layer, t, quant, rows, dim, off):
+    """The codes are those of the stored sum, in its own place and over x, by every kernel."""
+    g = np.random.default_rng(rows + dim)
+    x, xn = draw(g, (rows, dim + 2 * off), t)
+    res, rn = draw(g, (rows, dim + 2 * off), t, 2.0)
+    w, wn = draw(g, (dim,), "fp32")
+    at = np.s_[:, off: off + dim]
+    x, xn, res, rn = x[at], xn[at], res[at], rn[at]
+    f = layer.rmsnorm(x, w, residual=res, quant=quant, want_y=True, want_rstd=True)
+    r, y, rstd = R.norm(xn, rn, wn, float(np.float32(1e-5)), rounder(t))
+    c = norm_ops(dim) * R.U32                       # as above
+    assert np.array_equal(np64(f.r), r)
+    close("rstd", f.rstd, rstd, c * rstd)
+    close("y", f.y, y, (R.HALF[t] + c) * np.abs(y))
+    width = 128 if quant == "block" else dim
+    top = np.abs(y).reshape(rows, -1, width).max(-1)
+    close("scales", f.scales, top / 448, (c + 2 * R.U32) * top / 448)
+    code = f.y8.float().double().cpu().numpy()
+    want = y / np.repeat(top / 448, width, 1)
+    assert (np.abs(code - want) <= np.maximum(R.HALF["e4m3"] * np.abs(want), 2.0 ** -10) + (2 * c + 4 * R.U32) * np.abs(want)).all()
+    h = layer.rmsnorm(x, w, residual=res, quant=quant, r=x)
+    assert h.y is None and np.array_equal(np64(x), r)
+    assert torch.equal(h.y8.view(torch.uint8), f.y8.view(torch.uint8)) and torch.equal(h.scales, f.scales)
 
 
 @pytest.mark.parametrize("shape", [(2, 0, 512), (2, 3, 0, 64), (0, 4, 33)])
