@@ -58,6 +58,11 @@ def _like(shape, dtype, dev):
 _new = torch.empty_like
 
 
+def _rows_of(like, lengths):
+    """An output of which a call with ``lengths`` leaves rows unwritten: those are zeros."""
+    return _new(like) if lengths is None else torch.zeros_like(like)
+
+
 def _plan(key, make, *args):
     p = _PLANS.get(key)
     if p is None:
@@ -413,7 +418,7 @@ def _la_fwd_plan(q, k, v, log_decay, scale, state, lengths, out, state_out, rout
 
 def _la_fwd(p, st, q, k, v, log_decay, state, lengths, out, want_state, state_out, workspace):
     if out is None:
-        out = _new(p.likes[0])
+        out = _rows_of(p.likes[0], lengths)
     if state_out is None and want_state:
         state_out = _new(p.likes[1])
     ws, n, keep = _workspace(p, workspace)
@@ -430,8 +435,9 @@ def linattn(q, k, v, log_decay, scale=None, state=None, lengths=None, out=None, 
 
     q [B, L, H, dim_k], k [B, L, G, dim_k], v [B, L, G, dim_v] with H a multiple of G;
     ``scale`` defaults to dim_k ** -0.5; ``state`` fp32 [B, H, dim_k, dim_v] enters (default
-    zero); ``lengths`` int32 [B]: rows behind them count for nothing and are not written (``out``
-    keeps them).  ``state_out`` takes the final state (may be ``state``)."""
+    zero); ``lengths`` int32 [B]: rows behind them count for nothing and are not written (a given
+    ``out`` keeps them, a new one has zeros there).  ``state_out`` takes the final state (may be
+    ``state``)."""
     scale = None if scale is None else float(scale)
     p = _plan(("la", _sig(q), _sig(k), _sig(v), _sig(log_decay), scale, _sig(state), _sig(lengths), _sig(out),
                _sig(state_out), route),
@@ -447,11 +453,11 @@ def _la_bwd_plan(q, k, v, log_decay, do, scale, state, dstate, lengths, dq, dk, 
 
 def _la_bwd(p, st, q, k, v, log_decay, do, state, dstate, lengths, dq, dk, dv, workspace):
     if dq is None:
-        dq = _new(p.likes[2])
+        dq = _rows_of(p.likes[2], lengths)
     if dk is None:
-        dk = _new(p.likes[3])
+        dk = _rows_of(p.likes[3], lengths)
     if dv is None:
-        dv = _new(p.likes[4])
+        dv = _rows_of(p.likes[4], lengths)
     din = _new(p.likes[1])
     ws, n, keep = _workspace(p, workspace)
     rc = p.lib.ssm_linattn_bwd(p.desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
@@ -466,7 +472,8 @@ def linattn_backward(q, k, v, log_decay, do, scale=None, state=None, dstate=None
                      out=None, route=abi.LINATTN_AUTO, workspace=None, stream=None):
     """(dq, dk, dv, dstate): gradients of :func:`linattn` for ``do`` and ``dstate``, that of the
     final state (default zero); the returned dstate is that of the entering ``state``.
-    ``out``: buffers (dq, dk, dv), whose rows behind ``lengths`` stay as they are."""
+    ``out``: buffers (dq, dk, dv; each may be None), whose rows behind ``lengths`` stay as they
+    are; new ones have zeros there, so that a sum over a padded batch needs no mask."""
     dq, dk, dv = out if out is not None else (None, None, None)
     scale = None if scale is None else float(scale)
     p = _plan(("la'", _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(do), scale, _sig(state), _sig(dstate),

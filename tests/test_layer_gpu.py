@@ -463,6 +463,25 @@ def test_linattn_step(layer, t, B, H, G, dk, dv):
     close("state", S, rS, c * sb)
 
 
+@pytest.mark.parametrize("t,L,dim", [("bf16", 300, 64), ("fp32", 40, 24), ("bf16", 2600, 64)])
+def test_linattn_new_outputs_of_a_padded_batch(layer, t, L, dim):
+    """Outputs that a call makes have zeros behind the lengths, whatever was in their memory."""
+    T, _ = la_case(L, t, 3, L, 4, 2, dim, dim, True)
+    args = [T[x] for x in ("q", "k", "v", "log_decay")]
+    n = T["lengths"].tolist()
+    want = [torch.zeros(3, L, 4, dim, dtype=DT[t], device="cuda")] + [torch.zeros_like(T[x]) for x in ("q", "k", "v")]
+    layer.linattn(*args, lengths=T["lengths"], out=want[0])
+    layer.linattn_backward(*args, T["do"], lengths=T["lengths"], out=want[1:])
+    dirt = [torch.full_like(x, float("nan")) for x in want for _ in range(4)]      # blocks that the calls may get
+    del dirt
+    o, _ = layer.linattn(*args, lengths=T["lengths"])
+    got = [o, *layer.linattn_backward(*args, T["do"], lengths=T["lengths"])[:3]]
+    one = layer.linattn_backward(*args, T["do"], lengths=T["lengths"], out=(None, want[2].clone(), None))[:3]
+    for a, b in zip(got + list(one), want + want[1:]):
+        assert torch.equal(a, b)
+        assert all((a[i, n[i]:] == 0).all() for i in range(3))
+
+
 def test_linattn_empty_and_in_place(layer):
     g = np.random.default_rng(1)
     S, _ = draw(g, (2, 4, 64, 64), "fp32")
