@@ -410,8 +410,9 @@ SSM_API int ssm_cp_write_adjoint(const ssm_desc_t *d, const void *x, const void 
  * ---- The layer around the mixer ------------------------------------------------------
  * Operators a layer needs next to its scan.  They take their own small descriptors;
  * strides are element strides, the innermost dimension of every tensor is dense, inputs
- * may be broadcast (stride 0), outputs may not, and an output overlaps no input unless its
- * call says so.  Caller-owned memory, the caller's
+ * may be broadcast (stride 0), outputs may not, and an output overlaps no input and no other output
+ * unless its call says so (ssm_rope_* and ssm_linattn_* refuse one that begins at the other's address,
+ * or has its strides and a value of it).  Caller-owned memory, the caller's
  * stream and the error codes of the calls above; the descriptors' reserved fields must
  * be 0.  Nothing is launched for an empty problem (no rows, batch or tokens) except
  * where a call says what it then writes.

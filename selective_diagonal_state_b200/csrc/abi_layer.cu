@@ -85,6 +85,60 @@ int check_strides3(const char *name, const int64_t *s, const int64_t *extent, in
     return SSM_OK;
 }
 
+// A strided tensor of the call, for the checks that an output lies over nothing that other blocks
+// read.  `extent` rows of `inner` dense values.
+struct Span {
+    const char *name;
+    const void *p;
+    const int64_t *stride, *extent;
+    int64_t inner;
+    size_t es;
+};
+// Whether some of n_i s_i (|n_i| bounded by the two extents) and an offset within the rows come to d.
+// The dimensions in `order` have falling strides, each over all that the later ones span.
+bool meets(const Span &a, const Span &b, const int64_t *st, const int *order, int n, int64_t d) {
+    if (n == 0) return d < a.inner && d > -b.inner;
+    const int64_t s = st[order[0]];
+    int64_t q = d / s - (d % s < 0 ? 1 : 0);
+    for (int i = 0; i < 2; ++i, ++q)
+        if (q < a.extent[order[0]] && q > -b.extent[order[0]] && meets(a, b, st, order + 1, n - 1, d - q * s)) return true;
+    return false;
+}
+// Whether the two have a value in common: exact where their strides are the same (views of one
+// buffer, as of a projection's output), else only whether they begin at the same address.
+bool overlap(const Span &a, const Span &b) {
+    if (!a.p || !b.p) return false;
+    int64_t enda = a.inner, endb = b.inner, st[3];
+    bool same = a.es == b.es;
+    int order[3], n = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (a.extent[i] < 1 || b.extent[i] < 1) return false;
+        enda += (a.extent[i] - 1) * a.stride[i];
+        endb += (b.extent[i] - 1) * b.stride[i];
+        st[i] = a.extent[i] > 1 ? a.stride[i] : b.stride[i];
+        same = same && (a.extent[i] < 2 || b.extent[i] < 2 || a.stride[i] == b.stride[i]);
+        if ((a.extent[i] < 2 && b.extent[i] < 2) || st[i] == 0) continue;
+        int j = n++;
+        for (; j > 0 && st[order[j - 1]] < st[i]; --j) order[j] = order[j - 1];
+        order[j] = i;
+    }
+    const char *pa = (const char *)a.p, *pb = (const char *)b.p;
+    if (pa == pb) return true;
+    if (pa + enda * (int64_t)a.es <= pb || pb + endb * (int64_t)b.es <= pa || !same) return false;
+    const int64_t bytes = pb - pa, es = (int64_t)a.es;
+    return bytes % es != 0 || meets(a, b, st, order, n, bytes / es);
+}
+bool same_place(const Span &a, const Span &b) {
+    bool same = a.p == b.p;
+    for (int i = 0; i < 3; ++i) same = same && (a.extent[i] < 2 || a.stride[i] == b.stride[i]);
+    return same;
+}
+int apart(const Span &out, const Span &in) {
+    return overlap(out, in) ? fail(SSM_ERR_ARG, "%s lies over %s", out.name, in.name) : SSM_OK;
+}
+// the same for two dense arrays of n floats
+bool overlap(const float *a, const float *b, size_t n) { return a && b && a < b + n && b < a + n; }
+
 // ---- rmsnorm -------------------------------------------------------------------------
 int check_norm(const ssm_rmsnorm_desc_t *d) {
     if (!d) return fail(SSM_ERR_ARG, "descriptor is NULL");
@@ -145,6 +199,13 @@ int rope(const char *where, const ssm_rope_desc_t *d, const void *q, const void 
         (rc = need(freq, "freq", 8)) || (rc = may(positions, "positions", 8)))
         return rc;
     if (!has_q && !has_k) return SSM_OK;
+    const Span sq = {"q", has_q ? q : nullptr, d->stride_q, eq, d->headdim, es},
+               sk = {"k", has_k ? k : nullptr, d->stride_k, ek, d->headdim, es},
+               oq = {"q_out", has_q ? q_out : nullptr, d->stride_q_out, eq, d->headdim, es},
+               ok = {"k_out", has_k ? k_out : nullptr, d->stride_k_out, ek, d->headdim, es};
+    if ((!same_place(oq, sq) && (rc = apart(oq, sq))) || (!same_place(ok, sk) && (rc = apart(ok, sk))) ||
+        (rc = apart(oq, sk)) || (rc = apart(ok, sq)) || (rc = apart(oq, ok)))
+        return rc;
     return launched(where, stream, [&](cudaStream_t st) {
         return ssm::rope_rotate(*d, has_q ? q : nullptr, has_k ? k : nullptr, freq, positions, q_out,
                                 k_out, sign, st);
@@ -191,9 +252,20 @@ int la_inputs(const ssm_linattn_desc_t *d, const void *q, const void *k, const v
     return SSM_OK;
 }
 
+// `out` lies over none of the call's inputs (do_ may be null)
+int la_apart(const ssm_linattn_desc_t *d, const void *q, const void *k, const void *v, const void *do_, const Span &out) {
+    const int64_t eh[3] = {d->batch, d->seqlen, d->nheads}, eg[3] = {d->batch, d->seqlen, d->nheads_kv};
+    int rc;
+    if ((rc = apart(out, {"q", q, d->stride_q, eh, d->dim_k, out.es})) || (rc = apart(out, {"k", k, d->stride_k, eg, d->dim_k, out.es})) ||
+        (rc = apart(out, {"v", v, d->stride_v, eg, d->dim_v, out.es})) || (rc = apart(out, {"do", do_, d->stride_o, eh, d->dim_v, out.es})))
+        return rc;
+    return SSM_OK;
+}
+size_t state_floats(const ssm_linattn_desc_t *d) { return (size_t)(d->batch * d->nheads * d->dim_k * d->dim_v); }
+
 // copy of a state, or zeros
 cudaError_t state_copy(float *dst, const float *src, const ssm_linattn_desc_t *d, cudaStream_t st) {
-    const size_t n = sizeof(float) * (size_t)(d->batch * d->nheads * d->dim_k * d->dim_v);
+    const size_t n = sizeof(float) * state_floats(d);
     if (!dst || dst == src || n == 0) return cudaSuccess;
     return src ? cudaMemcpyAsync(dst, src, n, cudaMemcpyDeviceToDevice, st)
                : cudaMemsetAsync(dst, 0, n, st);
@@ -417,12 +489,15 @@ int ssm_linattn_fwd(const ssm_linattn_desc_t *d, const void *q, const void *k, c
     if ((rc = may(state_in, "state_in", 4)) || (rc = may(state_out, "state_out", 4)) ||
         (rc = may(lengths, "lengths", 4)) || (rc = may(o, "o", esize(d->dtype_io))))
         return rc;
+    if (state_out != state_in && overlap(state_out, state_in, state_floats(d)))
+        return fail(SSM_ERR_ARG, "state_out lies over a part of state_in");
     if (empty)
         return launched("ssm_linattn_fwd (empty)", stream,
                         [&](cudaStream_t st) { return state_copy(state_out, state_in, d, st); });
     if ((rc = la_inputs(d, q, k, v, log_decay))) return rc;
     const LaWs ws = la_layout(d, false);
     if ((rc = la_workspace("ssm_linattn_fwd", ws.total, workspace, workspace_bytes))) return rc;
+    if ((rc = la_apart(d, q, k, v, nullptr, {"o", o, d->stride_o, eh, d->dim_v, esize(d->dtype_io)}))) return rc;
     const int rep = (int)(d->nheads / d->nheads_kv), dk = (int)d->dim_k, dv = (int)d->dim_v;
     LaArgs p = la_args(d, log_decay, lengths);
     p.nwalk = 1;
@@ -448,7 +523,8 @@ int ssm_linattn_bwd(const ssm_linattn_desc_t *d, const void *q, const void *k, c
         return rc;
     if (dstate_in && (dstate_in == dstate_out || dstate_in == state_in))
         return fail(SSM_ERR_ARG, "dstate_in must be neither dstate_out nor state_in");
-    if (d->batch == 0 || d->seqlen == 0)
+    const bool over = overlap(dstate_in, dstate_out, state_floats(d)) || overlap(dstate_in, state_in, state_floats(d));
+    if (!over && (d->batch == 0 || d->seqlen == 0))
         return launched("ssm_linattn_bwd (empty)", stream,
                         [&](cudaStream_t st) { return state_copy(dstate_in, dstate_out, d, st); });
     const size_t es = esize(d->dtype_io);
@@ -457,6 +533,12 @@ int ssm_linattn_bwd(const ssm_linattn_desc_t *d, const void *q, const void *k, c
         return rc;
     const LaWs ws = la_layout(d, true);
     if ((rc = la_workspace("ssm_linattn_bwd", ws.total, workspace, workspace_bytes))) return rc;
+    const Span sdq = {"dq", dq, d->stride_dq, eh, d->dim_k, es}, sdk = {"dk", dk, d->stride_dk, eg, d->dim_k, es},
+               sdv = {"dv", dv, d->stride_dv, eg, d->dim_v, es};
+    if ((rc = la_apart(d, q, k, v, do_, sdq)) || (rc = la_apart(d, q, k, v, do_, sdk)) ||
+        (rc = la_apart(d, q, k, v, do_, sdv)) || (rc = apart(sdq, sdk)) || (rc = apart(sdq, sdv)) || (rc = apart(sdk, sdv)))
+        return rc;
+    if (over) return fail(SSM_ERR_ARG, "dstate_in lies over a part of dstate_out or state_in");
     const int rep = (int)(d->nheads / d->nheads_kv), ndk = (int)d->dim_k, ndv = (int)d->dim_v;
     const Operand oq = {q, d->stride_q, 1, ndk}, ok = {k, d->stride_k, rep, ndk},
                   ov = {v, d->stride_v, rep, ndv}, odo = {do_, d->stride_o, 1, ndv};
@@ -493,7 +575,8 @@ int ssm_linattn_step(const ssm_linattn_desc_t *d, const void *q, const void *k, 
     if ((rc = check_strides3("o", d->stride_o, eh, d->dim_v, true))) return rc;
     if (d->batch == 0) return SSM_OK;
     if ((rc = la_inputs(d, q, k, v, log_decay)) || (rc = need(state, "state", 4)) ||
-        (rc = need(o, "o", esize(d->dtype_io))))
+        (rc = need(o, "o", esize(d->dtype_io))) ||
+        (rc = la_apart(d, q, k, v, nullptr, {"o", o, d->stride_o, eh, d->dim_v, esize(d->dtype_io)})))
         return rc;
     return launched("ssm_linattn_step", stream, [&](cudaStream_t st) {
         return ssm::la_step(*d, q, k, v, log_decay, state, o, st);

@@ -360,7 +360,8 @@ def rope(q, k, freq, positions=None, layout="half", magnitude=1.0, q_out=None, k
 
     q, k: [batch, seqlen, heads, headdim] (either may be None); ``freq`` from
     :func:`rope_frequencies`; ``positions``: int64 [batch, seqlen] or [seqlen] (default 0, 1, ...);
-    ``layout``: "half" pairs value i with i + rot / 2, "pairs" neighbours; outputs may be the inputs."""
+    ``layout``: "half" pairs value i with i + rot / 2, "pairs" neighbours; ``q_out`` may be ``q`` itself
+    and ``k_out`` ``k``, and lie over nothing else of the call."""
     magnitude = float(magnitude)
     p = _plan(("rope", _sig(q), _sig(k), _sig(freq), _sig(positions), layout, magnitude, _sig(q_out), _sig(k_out)),
               _rope_plan, q, k, freq, positions, layout, magnitude, q_out, k_out)
@@ -435,7 +436,7 @@ def linattn(q, k, v, log_decay, scale=None, state=None, lengths=None, out=None, 
 
     q [B, L, H, dim_k], k [B, L, G, dim_k], v [B, L, G, dim_v] with H a multiple of G;
     ``scale`` defaults to dim_k ** -0.5; ``state`` fp32 [B, H, dim_k, dim_v] enters (default
-    zero); ``lengths`` int32 [B]: rows behind them count for nothing and are not written (a given
+    zero); ``out`` may not lie over q, k or v; ``lengths`` int32 [B]: rows behind them count for nothing and are not written (a given
     ``out`` keeps them, a new one has zeros there).  ``state_out`` takes the final state (may be
     ``state``)."""
     scale = None if scale is None else float(scale)
@@ -472,7 +473,7 @@ def linattn_backward(q, k, v, log_decay, do, scale=None, state=None, dstate=None
                      out=None, route=abi.LINATTN_AUTO, workspace=None, stream=None):
     """(dq, dk, dv, dstate): gradients of :func:`linattn` for ``do`` and ``dstate``, that of the
     final state (default zero); the returned dstate is that of the entering ``state``.
-    ``out``: buffers (dq, dk, dv; each may be None), whose rows behind ``lengths`` stay as they
+    ``out``: buffers (dq, dk, dv; each may be None) that lie over no input, whose rows behind ``lengths`` stay as they
     are; new ones have zeros there, so that a sum over a padded batch needs no mask."""
     dq, dk, dv = out if out is not None else (None, None, None)
     scale = None if scale is None else float(scale)
@@ -498,7 +499,8 @@ def _la_step(p, st, q, k, v, log_decay, state, out):
 
 
 def linattn_step(q, k, v, log_decay, state, scale=None, out=None, stream=None):
-    """o [B, 1, H, dim_v] of one token (seqlen 1); ``state`` is updated in place."""
+    """o [B, 1, H, dim_v] of one token (seqlen 1); ``state`` is updated in place; ``out`` may not lie
+    over q, k or v."""
     scale = None if scale is None else float(scale)
     p = _plan(("la1", _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(state), scale, _sig(out)),
               _la_step_plan, q, k, v, log_decay, state, scale, out)

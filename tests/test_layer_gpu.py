@@ -644,6 +644,32 @@ def test_helpers_refuse(layer):
     assert o.shape == z.shape and s is None
 
 
+def test_outputs_over_inputs_are_refused_and_beside_them_taken(layer):
+    g = np.random.default_rng(4)
+    buf, _ = draw(g, (2, 70, 16, 64), "bf16")
+    q, k, v, o = (buf[:, :, 4 * i: 4 * i + 4] for i in range(4))
+    dec = torch.tensor([-0.01, -0.1, -0.5, -1.0], device="cuda")
+    want, S = layer.linattn(q, k, v, dec)
+    got, S2 = layer.linattn(q, k, v, dec, out=o)
+    assert got is o and torch.equal(o, want) and torch.equal(S, S2)
+    do, _ = draw(g, (2, 70, 4, 64), "bf16")
+    for x in (q, k, v):
+        with pytest.raises(abi.SsmError, match="lies over"):
+            layer.linattn(q, k, v, dec, out=x)
+        with pytest.raises(abi.SsmError, match="lies over"):
+            layer.linattn_backward(q, k, v, dec, do, out=(x, None, None))
+        with pytest.raises(abi.SsmError, match="lies over"):
+            layer.linattn_step(q[:, :1], k[:, :1], v[:, :1], dec, S.clone(), out=x[:, :1])
+    with pytest.raises(abi.SsmError, match="lies over"):
+        layer.linattn(q, k, v, dec, out=buf[:, :, 10:14])
+    freq = layer.rope_frequencies(64)
+    with pytest.raises(abi.SsmError, match="lies over"):
+        layer.rope(q, k, freq, q_out=k, k_out=q)
+    a, b = layer.rope(q, k, freq)
+    layer.rope(q, k, freq, q_out=q, k_out=k)         # views of one buffer, in place
+    assert torch.equal(a, q) and torch.equal(b, k)
+
+
 # ---- together --------------------------------------------------------------------------
 
 def _block(layer, x, res, w, proj, freq, pos, dec, state=None, step=False):
