@@ -220,7 +220,7 @@ struct StepArgs {
 // 128 x 128 (137 MB there and back): 25.8 us on one B200, 5.2 TB/s, the launch among it.
 template <bool VEC>
 __global__ void __launch_bounds__(128) k_la_step(const StepArgs p, int slices) {
-    __shared__ float sq[LA_MAX_DIM], sk[LA_MAX_DIM], red[4][32];
+    __shared__ float sq[LA_MAX_DIM], sk[LA_MAX_DIM], red[4][32], decay[2];
     const int bh = blockIdx.x / slices, c0 = 32 * (blockIdx.x - bh * slices);
     const int b = bh / p.H, h = bh - b * p.H, hk = h / p.rep;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -228,33 +228,38 @@ __global__ void __launch_bounds__(128) k_la_step(const StepArgs p, int slices) {
         sq[a] = ld_io(p.q, b * p.sq0 + h * p.sq2 + a, p.bf16) * p.scale;
         sk[a] = ld_io(p.k, b * p.sk0 + hk * p.sk2 + a, p.bf16);
     }
-    const float lam = expf(p.log_decay[h]);
+    if (tid == 127) decay_pair(p.log_decay[h], decay[0], decay[1]);
     float *S = p.state + (long long)bh * p.dk * p.dv;
     const long long vb = b * p.sv0 + hk * p.sv2;
-    __syncthreads();
     if constexpr (VEC) {
         const int r0 = tid >> 3, c = c0 + 4 * (lane & 7);
         float v[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
         const bool on = c < p.dv;
-        if (on)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = ld_io(p.v, vb + c + j, p.bf16);
-        for (int a0 = 0; a0 < p.dk; a0 += 128) {
-            float4 x[8];
+        float4 x[8];
+        auto load = [&](int a0) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int a = a0 + r0 + 16 * i;
                 if (on && a < p.dk) x[i] = *reinterpret_cast<const float4 *>(S + (long long)a * p.dv + c);
             }
+        };
+        load(0);   // on its way beside the decay
+        if (on)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = ld_io(p.v, vb + c + j, p.bf16);
+        __syncthreads();
+        const float lam = decay[0], lam_lo = decay[1];
+        for (int a0 = 0; a0 < p.dk; a0 += 128) {
+            if (a0) load(a0);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int a = a0 + r0 + 16 * i;
                 if (!on || a >= p.dk) continue;
                 const float k = sk[a], q = sq[a];
-                x[i].x = fmaf(lam, x[i].x, k * v[0]);
-                x[i].y = fmaf(lam, x[i].y, k * v[1]);
-                x[i].z = fmaf(lam, x[i].z, k * v[2]);
-                x[i].w = fmaf(lam, x[i].w, k * v[3]);
+                x[i].x = fmaf(lam, x[i].x, fmaf(lam_lo, x[i].x, k * v[0]));
+                x[i].y = fmaf(lam, x[i].y, fmaf(lam_lo, x[i].y, k * v[1]));
+                x[i].z = fmaf(lam, x[i].z, fmaf(lam_lo, x[i].z, k * v[2]));
+                x[i].w = fmaf(lam, x[i].w, fmaf(lam_lo, x[i].w, k * v[3]));
                 o[0] = fmaf(q, x[i].x, o[0]);
                 o[1] = fmaf(q, x[i].y, o[1]);
                 o[2] = fmaf(q, x[i].z, o[2]);
@@ -270,19 +275,24 @@ __global__ void __launch_bounds__(128) k_la_step(const StepArgs p, int slices) {
         }
     } else {
         const int c = c0 + lane;
-        float o = 0.f;
-        if (c < p.dv) {
-            const float v = ld_io(p.v, vb + c, p.bf16);
-            for (int a0 = warp; a0 < p.dk; a0 += 64) {   // 16 rows on their way at once
-                float x[16];
+        float o = 0.f, x[16];
+        auto load = [&](int a0) {   // 16 rows on their way at once
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (a0 + 4 * i < p.dk) x[i] = S[(long long)(a0 + 4 * i) * p.dv + c];
+            for (int i = 0; i < 16; ++i)
+                if (c < p.dv && a0 + 4 * i < p.dk) x[i] = S[(long long)(a0 + 4 * i) * p.dv + c];
+        };
+        load(warp);
+        const float v = c < p.dv ? ld_io(p.v, vb + c, p.bf16) : 0.f;
+        __syncthreads();
+        const float lam = decay[0], lam_lo = decay[1];
+        if (c < p.dv) {
+            for (int a0 = warp; a0 < p.dk; a0 += 64) {
+                if (a0 > warp) load(a0);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int a = a0 + 4 * i;
                     if (a >= p.dk) break;
-                    x[i] = fmaf(lam, x[i], sk[a] * v);
+                    x[i] = fmaf(lam, x[i], fmaf(lam_lo, x[i], sk[a] * v));
                     o = fmaf(sq[a], x[i], o);
                     S[(long long)a * p.dv + c] = x[i];
                 }

@@ -482,6 +482,28 @@ def test_linattn_new_outputs_of_a_padded_batch(layer, t, L, dim):
         assert all((a[i, n[i]:] == 0).all() for i in range(3))
 
 
+@pytest.mark.parametrize("dv", [8, 7])
+def test_linattn_many_steps_forget_at_the_right_rate(layer, dv):
+    """2^14 steps with memories as long: the decay's own rounding (up to 2^-25) would be the same in every step
+    and add up, 2^14 2^-25 = 5e-4; without it only the steps' roundings do, two of at most 2^-24 each, which
+    have no common sign: 2 2^-24 2^7 = 1.5e-5 in the 2-norm."""
+    H, n = 8, 1 << 14
+    g = np.random.default_rng(dv)
+    dec = torch.from_numpy(-g.uniform(0.5, 1.5, H).astype(np.float32) / n).cuda()
+    k, v = torch.full((1, 1, H, 4), 0.75, device="cuda"), torch.full((1, 1, H, dv), 0.875, device="cuda")
+    S = torch.zeros(1, H, 4, dv, device="cuda")
+    out = torch.empty(1, 1, H, dv, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(64):
+            layer.linattn_step(k, k, v, dec, S, scale=1.0, out=out)
+    for _ in range(n // 64):
+        graph.replay()
+    lam = np.exp(dec.double().cpu().numpy())
+    want = np.broadcast_to((0.75 * 0.875 * (1 - lam ** n) / (1 - lam))[None, :, None, None], S.shape)
+    assert np.linalg.norm(np64(S) - want) <= 1.5e-5 * np.linalg.norm(want)
+
+
 def test_linattn_empty_and_in_place(layer):
     g = np.random.default_rng(1)
     S, _ = draw(g, (2, 4, 64, 64), "fp32")
