@@ -9,6 +9,9 @@
 
 namespace ssm {
 
+// Streaming multiprocessors of a B200, in the rules that also size workspaces: those must give the same
+// whichever device is current when a caller asks for the size.  Grids alone go by sm_count().
+constexpr int SMS = 148;
 int sm_count();
 void profile_mark(cudaStream_t st, const char *name);
 long long abi_wait_limit();   // ssm_scan_set_wait_limit's

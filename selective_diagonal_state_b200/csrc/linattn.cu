@@ -338,7 +338,7 @@ cudaError_t la_group_sum(const float *in, void *out, const long long *so, int B,
         return cudaGetLastError();
     }
     long long blocks = (total + 255) / 256;
-    if (blocks > 148 * 16) blocks = 148 * 16;
+    if (blocks > sm_count() * 16ll) blocks = sm_count() * 16ll;
     k_la_group_sum<<<(unsigned)blocks, 256, 0, st>>>(in, out, so[0], so[1], so[2], B, L, H, rep, d,
                                                      lengths, bf16);
     profile_mark(st, "k_la_group_sum");

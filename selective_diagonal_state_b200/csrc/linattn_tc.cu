@@ -879,13 +879,13 @@ bool la_chunked_sizes(int bf16, int da, int dc) { return bf16 && da <= 128 && da
 // Segments of the sequences (of `L` tokens; `items` blocks without segments): the count with
 // the shortest estimate, in chunks of a walk (about 2.5 us): a block takes 3 to begin and end,
 // a chunk whose state alone is walked 0.7, the pass over the segments' states and its launch
-// 3, and 148 blocks run at a time.
+// 3, and a block an SM runs at a time.
 int la_segments(long long L, long long items) {
     const long long nc = (L + la::C - 1) / la::C;
     double best = 0;
     int pick = 1;
     for (long long n = 1; n <= nc && n <= 64; ++n) {
-        const long long g = (nc + n - 1) / n, seg = (nc + g - 1) / g, waves = (items * seg + 147) / 148;
+        const long long g = (nc + n - 1) / n, seg = (nc + g - 1) / g, waves = (items * seg + SMS - 1) / SMS;
         const double t = waves * (g + 3.0) + (seg > 1 ? waves * (0.7 * g + 3.0) + 3.0 : 0.0);
         if (seg == n && (n == 1 || t < 0.95 * best)) {
             best = t;

@@ -11,7 +11,8 @@
 // bytes a lane and tensor in flight.  On one B200, 65536 x 2048 bf16 with a residual: 160 us without
 // codes (1.07 GB, 6.7 TB/s), 152 with a row scale (0.94 GB, 6.2 TB/s; 206 with a block a
 // row), 178 with block scales, whose maxima go through shuffles; the gradient 232 us
-// (1.07 GB, 4.6 TB/s: the sums of dweight in registers leave a third of the warps).
+// (1.07 GB, 4.6 TB/s: three tensors and the sums of dweight take all of a thread's 128 registers and, at four
+// pieces of bf16, 200 bytes of spills, so that one block of 16 warps is on an SM, a quarter of its warps).
 // With few rows, a decoding step's, a block takes a row, for the shortest chain (8 x 2048: 2.4 us).
 #include <cuda_fp8.h>
 
@@ -444,12 +445,13 @@ bool al16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
 // Pieces a thread and threads a row for rows of nv 16-byte pieces; v 0: the kernels for any
 // row.  Forward: a warp a row while eight pieces a lane suffice, wider teams above; a block a row where
-// there are too few rows for that to fill the card (four warps an SM).
+// there are too few rows for that to fill the card (four warps an SM): 591 x 2048 with block scales took 4.2 us
+// so and 8.0 with a warp a row, 8 x 2048 4.2 and 6.3 (in a graph), 3999 x 1024 12.4 and 8.3.
 struct Shape {
     int v, t;
 };
 Shape fwd_team(int nv, long long rows) {
-    if (rows < 148 * 4 && nv > 32) {
+    if (rows < SMS * 4 && nv > 32) {
         if (nv <= 256) return {1, 256};
         if (nv <= 512) return {2, 256};
         if (nv <= 1024) return {4, 256};
@@ -463,7 +465,9 @@ Shape fwd_team(int nv, long long rows) {
     if (nv <= 2048) return {8, 256};
     return {0, 0};
 }
-// Backward: three tensors and the sums of dweight are in registers, so half of that.
+// Backward: three tensors and the sums of dweight are in registers, so half of that.  Four pieces of
+// bf16 spill; where three do (129 to 192 of them), 8191 rows of 1032 to 1536 take 20.6 to 22.7 us, 65536 110 to 122,
+// against 33 to 37 and 192 to 214 with four.
 Shape bwd_team(int nv) {
     if (nv <= 32) return {1, 32};
     if (nv <= 64) return {2, 32};
@@ -476,7 +480,7 @@ Shape bwd_team(int nv) {
     return {0, 0};
 }
 
-constexpr int DW_BLOCKS = 148;   // partial sums of dweight: a block an SM
+constexpr int DW_BLOCKS = SMS;   // partial sums of dweight: a block an SM
 
 int bwd_blocks(const ssm_rmsnorm_desc_t &d) {
     const int n = d.dtype_io == SSM_BF16 ? 8 : 4;
