@@ -193,6 +193,8 @@ def _rows(t, name, dim):
 
 def _norm_plan(like, eps, quant, weight, dev, **tensors):
     """``like``: the tensor whose shape and type all others have; outputs not named are dense."""
+    if like.dim() == 0:
+        raise ValueError("the norm runs over a last dimension: x has none")
     dim = like.shape[-1]
     if weight is not None:
         _want(weight, "weight", (dim,), torch.float32, True)
@@ -400,7 +402,7 @@ def _la_plan(which, q, k, v, log_decay, lengths, scale, route, states, more):
             _want(t, name, size, torch.float32, True)
     d = p.desc = abi.LinattnDesc()
     d.batch, d.seqlen, d.nheads, d.nheads_kv, d.dim_k, d.dim_v = b, L, h, g, dk, dv
-    d.scale, d.dtype_io, d.route = dk ** -0.5 if scale is None else scale, _io(q, "q"), route
+    d.scale, d.dtype_io, d.route = max(dk, 1) ** -0.5 if scale is None else scale, _io(q, "q"), route
     d.stride_q[:], d.stride_k[:], d.stride_v[:] = q.stride()[:3], k.stride()[:3], v.stride()[:3]
     for name, t, shape in more:
         if t is not None:

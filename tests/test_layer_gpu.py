@@ -33,6 +33,13 @@ def layer():
     return layer
 
 
+@pytest.fixture(autouse=True)
+def _no_wait_gave_up():
+    """A bounded wait that gives up is reported behind the call only."""
+    yield
+    abi.ssm_scan_poll_device_error()
+
+
 def rounder(t):
     return lambda a: torch.from_numpy(np.asarray(a)).to(torch.float32).to(DT[t]).double().numpy()
 
@@ -664,6 +671,31 @@ def test_helpers_refuse(layer):
     z = q[:, :0]
     o, s = layer.linattn(z, z, z, dec, want_state=False)      # nothing to write is no error
     assert o.shape == z.shape and s is None
+
+
+def test_helpers_refuse_what_has_no_last_dimension(layer):
+    with pytest.raises(ValueError, match="last dimension"):
+        layer.rmsnorm(torch.zeros((), device="cuda"))
+    with pytest.raises(abi.SsmError, match="dim"):
+        layer.rmsnorm(torch.zeros(3, 0, device="cuda"))
+    z, dec = torch.zeros(1, 4, 2, 0, device="cuda"), torch.zeros(2, device="cuda")
+    v = torch.zeros(1, 4, 2, 8, device="cuda")
+    with pytest.raises(abi.SsmError, match="dim_k"):
+        layer.linattn(z, z, v, dec)
+    with pytest.raises(abi.SsmError, match="headdim"):
+        layer.rope(z, z, torch.zeros(0, dtype=torch.float64, device="cuda"))
+
+
+def test_streams_given_as_numbers(layer):
+    g = np.random.default_rng(7)
+    x, _ = draw(g, (5, 200), "bf16")
+    want = layer.rmsnorm(x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for st in (s, s.cuda_stream, 0, torch.cuda.default_stream()):
+        got = layer.rmsnorm(x, stream=st)
+        torch.cuda.synchronize()
+        assert torch.equal(got.y, want.y)
 
 
 def test_outputs_over_inputs_are_refused_and_beside_them_taken(layer):
