@@ -535,7 +535,9 @@ SSM_API int ssm_rope_bwd(const ssm_rope_desc_t *d, const void *dq, const void *d
  * after its first lengths[b] tokens (clamped to 0 .. seqlen): the rows behind them count for
  * nothing, whatever they hold, and those of the outputs are left as they were.  dim_k and dim_v up to 256.
  * The decays are constants of the head and have no gradient; a learned, per-token
- * decay is ssm_scan_*.  A value that is not finite in a token of the sequence may reach every
+ * decay is ssm_scan_*, which computes the same recurrence where dt is 1, with queries and keys (C, B) that
+ * groups of heads share and values of each head; here each head has queries of its own over keys and values
+ * that heads may share, and the rows of a batch have lengths.  A value that is not finite in a token of the sequence may reach every
  * output of its batch row and head.
  */
 typedef struct ssm_linattn_desc {
@@ -551,8 +553,11 @@ typedef struct ssm_linattn_desc {
 /* SSM_LINATTN_AUTO: the tensor-core walk over 128-token chunks where it applies (bf16,
  * head dims that are multiples of 8, dim_k at most 128 and for the gradient dim_v too, 16-byte
  * aligned tensors and strides, and more than 2048 / max(dim_k, dim_v) tokens), else the
- * token-by-token recurrence; SSM_LINATTN_RECURRENT: always the latter.  Results are equal up
- * to rounding. */
+ * token-by-token recurrence; SSM_LINATTN_RECURRENT: always the latter, at many times the time.  The walk
+ * rounds the scores and the state that outputs are read from to bf16 once, which is about what one more
+ * rounding of its inputs does: o, dq, dk and dv in bf16 are 2.3e-3 from exact values (2-norm, relative),
+ * the recurrence's 1.7e-3, which the rounding of the stored values alone takes.  States and their gradients
+ * keep 24 bits by either. */
 enum ssm_linattn_route { SSM_LINATTN_AUTO = 0, SSM_LINATTN_RECURRENT = 1 };
 
 /* Bytes of device workspace (256-byte aligned, contents arbitrary) that ssm_linattn_fwd

@@ -25,7 +25,7 @@
 // so that P, V', the state and the output of one chunk are made beside the products of others.
 //
 // On one B200, 4 x 16384 tokens of 16 heads of 128 / 128: 319 us, 1.08 GB (3.4 TB/s) and 0.5
-// PFLOP/s; 4 x 4096 tokens of 16 heads over 4: 87 us, the gradient 312; 1 x 257: 14 us.  What bounds
+// PFLOP/s (384 us call behind call for two seconds: at 1000 W the SMs run at 1550 MHz); 4 x 4096 tokens of 16 heads over 4: 87 us, the gradient 312; 1 x 257: 14 us.  What bounds
 // it is none of the units (tensor pipe 26 %, issue 47 %, HBM 26 %) but the steps of a chunk handed on
 // from role to role, 2.5 us a chunk: scores, P, P V, output, and K^T V', state, A S.  Taking the
 // output off the first of these chains (P a chunk ahead of it, two accumulators) was no faster, 328 us.
