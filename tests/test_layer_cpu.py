@@ -246,8 +246,8 @@ def test_states_of_the_gradient_may_not_be_shared(lib):
 
 
 def test_outputs_over_inputs_are_refused(lib):
-    """By address or, with the same strides, by any value in common; views of one buffer side by side are
-    not (they get as far as the launch, which fails without a device)."""
+    """By address or, with the same strides, by any value in common.  (What is taken, views of one buffer
+    side by side among it, is launched, and so tested with real buffers on a GPU.)"""
     E = 2                                     # bytes a value
     at = lambda i: FAKE + E * i               # noqa: E731
     d = la_desc(g=4)                          # [2, 8, 4, 64] each
@@ -261,16 +261,13 @@ def test_outputs_over_inputs_are_refused(lib):
         for off in (0, 63, -63, 64, row, -row, n - 1, 1 - n):
             rc = fwd(d, *far, far[i] + E * off)
             assert rc == -1 and "o lies over " + name in err(lib), (name, off)
-    assert fwd(d, *far, at(6 * n)) not in (0, -1) and fwd(d, *far, at(n)) not in (0, -1)
     w = la_desc(g=4)                          # q, k, v and o side by side in rows of 16 heads
     for f in ("stride_q", "stride_k", "stride_v", "stride_o"):
         getattr(w, f)[:] = 8 * 16 * 64, 16 * 64, 64
     side = [at(4 * 64 * i) for i in range(4)]
-    assert fwd(w, *side) not in (0, -1)
     assert fwd(w, *side[:3], side[2] + E * 64) == -1 and "over v" in err(lib)        # three of v's heads
     assert fwd(w, *side[:3], side[3] + E * 64) == -1 and "over q" in err(lib)        # the next token's q
     assert fwd(d, *far, at(6 * n), si=FAKE + (1 << 30), so=FAKE + (1 << 30) + 4) == -1 and "state_out" in err(lib)
-    assert fwd(d, *far, at(6 * n), si=FAKE + (1 << 30), so=FAKE + (1 << 30)) not in (0, -1)
     names = ["q", "k", "v", "log_decay", "state_in", "lengths", "do", "dstate_out", "dq", "dk", "dv", "dstate_in"]
     ok = dict(zip(names, [at(2 * n * i) for i in range(12)])) | dict(state_in=FAKE + (1 << 30), lengths=None,
                                                                      dstate_out=FAKE + (2 << 30), dstate_in=FAKE + (3 << 30))
@@ -278,7 +275,6 @@ def test_outputs_over_inputs_are_refused(lib):
     def bwd(**kw):
         return lib.ssm_linattn_bwd(d, *[(ok | kw)[x] for x in names], None, 0, None)
 
-    assert bwd() not in (0, -1)
     for out in ("dq", "dk", "dv"):
         for over in ("q", "k", "v", "do"):
             assert bwd(**{out: ok[over]}) == -1 and f"{out} lies over {over}" in err(lib)
@@ -292,8 +288,6 @@ def test_outputs_over_inputs_are_refused(lib):
     def rope(d, q, k, qo, ko):
         return lib.ssm_rope_fwd(d, q, k, FAKE, None, qo, ko, None)
 
-    assert rope(r, far[0], far[1], far[0], far[1]) not in (0, -1)          # in place
-    assert rope(r, far[0], far[1], far[2], at(6 * n)) not in (0, -1)
     assert rope(r, far[0], far[1], far[1], far[0]) == -1 and "q_out lies over k" in err(lib)
     assert rope(r, far[0], far[1], far[0] + E * row, far[1]) == -1 and "over q" in err(lib)
     assert rope(r, far[0], far[1], far[2], far[2] + E) == -1 and "k_out" in err(lib)

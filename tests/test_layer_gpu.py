@@ -707,6 +707,10 @@ def test_outputs_over_inputs_are_refused_and_beside_them_taken(layer):
     got, S2 = layer.linattn(q, k, v, dec, out=o)
     assert got is o and torch.equal(o, want) and torch.equal(S, S2)
     do, _ = draw(g, (2, 70, 4, 64), "bf16")
+    wide = torch.zeros(2, 70, 13, 64, dtype=torch.bfloat16, device="cuda")       # the gradients side by side, shifted
+    back = layer.linattn_backward(q, k, v, dec, do)
+    layer.linattn_backward(q, k, v, dec, do, out=(wide[:, :, 9:], wide[:, :, 1:5], wide[:, :, 5:9]))
+    assert (wide[:, :, 0] == 0).all() and torch.equal(wide[:, :, 1:], torch.cat([back[1], back[2], back[0]], 2))
     for x in (q, k, v):
         with pytest.raises(abi.SsmError, match="lies over"):
             layer.linattn(q, k, v, dec, out=x)
