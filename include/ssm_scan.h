@@ -411,8 +411,8 @@ SSM_API int ssm_cp_write_adjoint(const ssm_desc_t *d, const void *x, const void 
  * Operators a layer needs next to its scan.  They take their own small descriptors;
  * strides are element strides, the innermost dimension of every tensor is dense, inputs
  * may be broadcast (stride 0), outputs may not, and an output overlaps no input and no other output
- * unless its call says so (ssm_rope_* and ssm_linattn_* refuse one that begins at the other's address,
- * or has its strides and a value of it).  Caller-owned memory, the caller's
+ * unless its call says so: one that begins at the other's address, or has its strides and a value
+ * of it, is refused.  Caller-owned memory, the caller's
  * stream and the error codes of the calls above; the descriptors' reserved fields must
  * be 0.  Nothing is launched for an empty problem (no rows, batch or tokens) except
  * where a call says what it then writes.
@@ -441,7 +441,7 @@ typedef struct ssm_rmsnorm_desc {
  *     r = x + residual            (rounded to dtype_io; r = x without a residual)
  *     rstd = 1 / sqrt(mean(r^2) + eps),   y = r rstd w
  * x and residual are read, r (may be NULL without a residual) receives the sum, which
- * may overwrite x or residual.  weight is fp32 [dim] (NULL: ones).  With SSM_QUANT_NONE y
+ * may overwrite x or residual (the same address and stride).  weight is fp32 [dim] (NULL: ones).  With SSM_QUANT_NONE y
  * receives the result in dtype_io.  Otherwise y8 receives e4m3 codes and scales (fp32
  * [rows][1] or [rows][dim / 128], dense) the scale of each row or block:
  *     scale = max|y| / 448,   code = e4m3(y 448 / max|y|)     (y in fp32, not rounded first)

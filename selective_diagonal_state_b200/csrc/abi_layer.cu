@@ -139,6 +139,10 @@ int apart(const Span &out, const Span &in) {
 // the same for two dense arrays of n floats
 bool overlap(const float *a, const float *b, size_t n) { return a && b && a < b + n && b < a + n; }
 
+// the same, but each may be the other: rows that lie in one another's place are read before they are
+// written, by one team
+int apart_or_same(const Span &out, const Span &in) { return same_place(out, in) ? SSM_OK : apart(out, in); }
+
 // ---- rmsnorm -------------------------------------------------------------------------
 int check_norm(const ssm_rmsnorm_desc_t *d) {
     if (!d) return fail(SSM_ERR_ARG, "descriptor is NULL");
@@ -203,8 +207,7 @@ int rope(const char *where, const ssm_rope_desc_t *d, const void *q, const void 
                sk = {"k", has_k ? k : nullptr, d->stride_k, ek, d->headdim, es},
                oq = {"q_out", has_q ? q_out : nullptr, d->stride_q_out, eq, d->headdim, es},
                ok = {"k_out", has_k ? k_out : nullptr, d->stride_k_out, ek, d->headdim, es};
-    if ((!same_place(oq, sq) && (rc = apart(oq, sq))) || (!same_place(ok, sk) && (rc = apart(ok, sk))) ||
-        (rc = apart(oq, sk)) || (rc = apart(ok, sq)) || (rc = apart(oq, ok)))
+    if ((rc = apart_or_same(oq, sq)) || (rc = apart_or_same(ok, sk)) || (rc = apart(oq, sk)) || (rc = apart(ok, sq)) || (rc = apart(oq, ok)))
         return rc;
     return launched(where, stream, [&](cudaStream_t st) {
         return ssm::rope_rotate(*d, has_q ? q : nullptr, has_k ? k : nullptr, freq, positions, q_out,
@@ -390,6 +393,13 @@ int ssm_rmsnorm_fwd(const ssm_rmsnorm_desc_t *d, const void *x, const void *resi
         (rc = q ? may(y, "y", es) : need(y, "y", es)) || (rc = may(rstd, "rstd", 4)))
         return rc;
     if (q && ((rc = need(y8, "y8", 1)) || (rc = need(scales, "scales", 4)))) return rc;
+    const int64_t rows[3] = {d->rows, 1, 1}, ix[3] = {d->stride_x}, ires[3] = {d->stride_residual}, ir[3] = {d->stride_r},
+                  iy[3] = {d->stride_y};
+    const Span sx = {"x", x, ix, rows, d->dim, es}, sres = {"residual", residual, ires, rows, d->dim, es},
+               sr = {"r", r, ir, rows, d->dim, es}, sy = {"y", y, iy, rows, d->dim, es};
+    if ((rc = apart_or_same(sr, sx)) || (rc = apart_or_same(sr, sres)) || (rc = apart_or_same(sy, sx)) ||
+        (rc = apart_or_same(sy, sres)) || (rc = apart(sy, sr)))
+        return rc;
     return launched("ssm_rmsnorm_fwd", stream, [&](cudaStream_t st) {
         return ssm::rmsnorm_forward(*d, x, residual, weight, r, y, q ? y8 : nullptr, scales, rstd, st);
     });
@@ -423,6 +433,12 @@ int ssm_rmsnorm_bwd(const ssm_rmsnorm_desc_t *d, const void *dy, const void *r, 
         return rc;
     if (dweight && (rc = la_workspace("ssm_rmsnorm_bwd", ssm::rmsnorm_bwd_bytes(*d), workspace,
                                       workspace_bytes)))
+        return rc;
+    const int64_t rows[3] = {d->rows, 1, 1}, idy[3] = {d->stride_dy}, ir[3] = {d->stride_r}, idr[3] = {d->stride_dr},
+                  idx[3] = {d->stride_dx};
+    const Span sdx = {"dx", dx, idx, rows, d->dim, es};
+    if ((rc = apart_or_same(sdx, {"dy", dy, idy, rows, d->dim, es})) || (rc = apart_or_same(sdx, {"r", r, ir, rows, d->dim, es})) ||
+        (rc = apart_or_same(sdx, {"dr", dr, idr, rows, d->dim, es})))
         return rc;
     return launched("ssm_rmsnorm_bwd", stream, [&](cudaStream_t st) {
         return ssm::rmsnorm_backward(*d, dy, r, weight, rstd, dr, dx, dweight, (float *)workspace, st);

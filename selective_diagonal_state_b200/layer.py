@@ -249,7 +249,7 @@ def rmsnorm(x, weight=None, residual=None, eps=1e-5, quant=None, want_y=None, wa
 
     ``quant``: None, "row" or "block" (128 columns) for e4m3 codes with scales; ``want_y``: also
     the unquantised norm (default: only without ``quant``); ``want_rstd`` for a later
-    :func:`rmsnorm_backward`; ``r``: where the sum goes (may be ``x`` or ``residual``)."""
+    :func:`rmsnorm_backward`; ``r``: where the sum goes (may be ``x`` or ``residual`` itself)."""
     eps = float(eps)
     p = _plan(("norm", _sig(x), _sig(weight), _sig(residual), _sig(r), eps, quant, want_y),
               _norm_fwd_plan, x, weight, residual, r, eps, quant, want_y)
@@ -282,7 +282,8 @@ def _norm_bwd(p, st, dy, r, weight, rstd, dr, dx, want_dweight, workspace):
 def rmsnorm_backward(dy, r, weight, rstd, dr=None, dx=None, want_dweight=None, workspace=None,
                      stream=None):
     """(dx, dweight) for ``dy``, the gradient of the norm, and ``dr``, that of the residual
-    stream behind it; ``r`` and ``rstd`` as :func:`rmsnorm` returned them.  dx is the gradient
+    stream behind it; ``r`` and ``rstd`` as :func:`rmsnorm` returned them; ``dx`` may be ``dy`` or ``dr``
+    itself.  dx is the gradient
     of ``x`` and of ``residual``; dweight (fp32) is None without a weight."""
     p = _plan(("norm'", _sig(dy), _sig(r), _sig(weight), _sig(rstd), _sig(dr), _sig(dx)),
               _norm_bwd_plan, dy, r, weight, rstd, dr, dx)

@@ -283,6 +283,24 @@ def test_outputs_over_inputs_are_refused(lib):
     assert bwd(dstate_in=ok["dstate_out"] + 16) == -1 and "dstate" in err(lib)
     one = la_desc(seqlen=1, g=4)
     assert lib.ssm_linattn_step(one, *far, FAKE, FAKE + (1 << 30), far[2], None) == -1 and "over v" in err(lib)
+    x, y8, scales, rstd = (FAKE + (i << 30) for i in range(4))      # 4 rows of 256
+    m, far = norm_desc(), FAKE + (5 << 30)
+
+    def norm(d, r, y=far, res=FAKE + (6 << 30)):
+        return lib.ssm_rmsnorm_fwd(d, x, res, None, r, y, y8, scales, rstd, None)
+
+    for off in (1, -1, 255, 256, -256, 1023):
+        assert norm(m, x + E * off) == -1 and "r lies over x" in err(lib)
+        assert norm(m, far, far + E * off) == -1 and "y lies over r" in err(lib)
+        assert norm(m, far, x + E * off) == -1 and "y lies over x" in err(lib)
+        assert norm(m, far + E * off, far + (1 << 25), far) == -1 and "r lies over residual" in err(lib)
+        b = [far, x, FAKE, rstd, far + (1 << 26)]
+        for i, name in ((0, "dy"), (1, "r"), (4, "dr")):
+            assert lib.ssm_rmsnorm_bwd(m, *b[:2], None, rstd, b[4], b[i] + E * off, None, None, 0, None) == -1
+            assert "dx lies over " + name in err(lib)
+    assert norm(m, far, far) == -1 and "y lies over r" in err(lib)
+    assert norm(norm_desc(stride_r=512), x) == -1 and "r lies over x" in err(lib)     # in place, another stride
+    far = (at(0), at(2 * n), at(4 * n))
     r = rope_desc(hq=4, hk=4)
 
     def rope(d, q, k, qo, ko):
